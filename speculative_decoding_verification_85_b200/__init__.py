@@ -16,6 +16,9 @@ from ._binding import (  # noqa: F401
     spec_verify_shard_stats, spec_verify_vocab_sharded, staging_size, vocab_shards,
     workspace_size,
 )
+from ._tree import (  # noqa: F401
+    MAX_NODES, kv_append, kv_slots, spec_verify_probs, spec_verify_tree,
+)
 
 __all__ = [
     "spec_verify", "spec_verify_multidraft", "spec_verify_host", "Verifier", "workspace_size",
@@ -24,4 +27,5 @@ __all__ = [
     "spec_verify_shard_stats", "spec_verify_shard_decide", "spec_verify_shard_pick",
     "spec_verify_vocab_sharded", "vocab_shards", "shard_stats_bytes", "shard_candidate_bytes",
     "gather_records", "SHARD_ALIGN",
+    "spec_verify_probs", "spec_verify_tree", "kv_slots", "kv_append", "MAX_NODES",
 ]
