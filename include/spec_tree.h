@@ -177,6 +177,51 @@ typedef struct {
 } sv_kv_append_args;
 int spec_kv_append(const sv_kv_append_args* args, void* stream);
 
+/*
+ * spec_tree_attention -- softmax attention of drafted nodes.
+ *
+ * Node i of sequence b, query head h (key head h / (Hq / Hkv)) attends to the
+ * lens[b] cached tokens of its sequence and to itself and its ancestors:
+ *   out[i, h] = sum_t softmax_t(scale q_i . k_t) v_t.
+ * Inputs (device):
+ *   q [N, Hq, D], k, v [N, Hkv, D]: the nodes' rows (packed as cu_nodes says).
+ *   k_cache, v_cache [num_pages, page_size, Hkv, D]: the pages.
+ *   block_table [B, table_width] int32 (row stride table_row): request b's
+ *   token t lies in page block_table[b][t / page_size].
+ *   lens [B] int32 (>= 0), parents [N], cu_nodes [B + 1] int32.
+ * Outputs: out [N, Hq, D], dense; out_lse [N, Hq] fp32 or NULL: the natural
+ * logarithm of the sum of exp(scale q . k).  Rows outside every sequence are
+ * left as they were.
+ * Types: SV_BF16 or SV_F16 throughout.  D a multiple of 8 up to
+ * SV_MAX_HEAD_DIM, Hq a multiple of Hkv, Hq / Hkv <= 128; page_size 8, 16,
+ * 32, 64 or a multiple of 128; strides (elements) multiples of 8, addresses
+ * 16-byte aligned.  Products are accumulated in fp32, the softmax is fp32,
+ * its weights are rounded to the input type for the second product.
+ * Nothing a node may not see reaches its result, whatever it holds (other
+ * branches, rest of the last page, neighbours' rows: infinities and NaN too).
+ * Marks: a sequence whose lens is negative or beyond its table row, which
+ * has more than SV_MAX_NODES nodes, or one of whose pages (of those it uses)
+ * lies outside [0, num_pages), gets NaN in its rows; so does a node one of
+ * whose ancestors (itself included) has a parent outside [-1, own index).
+ * The rows of a sequence whose cu_nodes bounds do not lie in [0, N] are left
+ * as they were.
+ * Workspace: spec_tree_attention_workspace_size bytes, 256-byte aligned, of
+ * any content; nothing is kept in it between calls.
+ */
+typedef struct {
+  const void *q, *k, *v, *k_cache, *v_cache;
+  void* out;
+  float* out_lse;
+  const int32_t *block_table, *lens, *parents, *cu_nodes;
+  int64_t q_node, q_head, k_node, k_head, v_node, v_head;
+  int64_t kc_page, kc_token, kc_head, vc_page, vc_token, vc_head, table_row;
+  int B, N, Hq, Hkv, D, num_pages, page_size, table_width, dtype;
+  float scale;
+} sv_tree_attention_args;
+size_t spec_tree_attention_workspace_size(int Hq, int Hkv, int D);
+int spec_tree_attention(const sv_tree_attention_args* args, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,7 +17,8 @@ from ._binding import (  # noqa: F401
     workspace_size,
 )
 from ._tree import (  # noqa: F401
-    MAX_NODES, kv_append, kv_slots, spec_verify_probs, spec_verify_tree,
+    MAX_NODES, kv_append, kv_slots, spec_verify_probs, spec_verify_tree, tree_attention,
+    tree_attention_workspace_size,
 )
 
 __all__ = [
@@ -28,4 +29,5 @@ __all__ = [
     "spec_verify_vocab_sharded", "vocab_shards", "shard_stats_bytes", "shard_candidate_bytes",
     "gather_records", "SHARD_ALIGN",
     "spec_verify_probs", "spec_verify_tree", "kv_slots", "kv_append", "MAX_NODES",
+    "tree_attention", "tree_attention_workspace_size",
 ]

@@ -22,6 +22,17 @@ class _AppendArgs(C.Structure):
                 ("num_pages", _i32), ("page_size", _i32), ("elem_bytes", _i32)]
 
 
+class _AttentionArgs(C.Structure):
+    _fields_ = ([(n, _vp) for n in ("q", "k", "v", "k_cache", "v_cache", "out", "out_lse",
+                                    "block_table", "lens", "parents", "cu_nodes")]
+                + [(n, _i64) for n in ("q_node", "q_head", "k_node", "k_head", "v_node", "v_head",
+                                       "kc_page", "kc_token", "kc_head", "vc_page", "vc_token",
+                                       "vc_head", "table_row")]
+                + [(n, _i32) for n in ("B", "N", "Hq", "Hkv", "D", "num_pages", "page_size",
+                                       "table_width", "dtype")]
+                + [("scale", C.c_float)])
+
+
 _ready = None
 
 
@@ -39,6 +50,10 @@ def _lib():
         L.spec_kv_slots.restype = _i32
         L.spec_kv_append.argtypes = [C.POINTER(_AppendArgs), _vp]
         L.spec_kv_append.restype = _i32
+        L.spec_tree_attention_workspace_size.argtypes = [_i32, _i32, _i32]
+        L.spec_tree_attention_workspace_size.restype = C.c_size_t
+        L.spec_tree_attention.argtypes = [C.POINTER(_AttentionArgs), _vp, C.c_size_t, _vp]
+        L.spec_tree_attention.restype = _i32
         _ready = L
     return L
 
@@ -230,3 +245,62 @@ def kv_append(k, v, slots, k_cache, v_cache, *, stream=None):
         a.cache_page[w], a.cache_token[w], a.cache_head[w] = cache.stride()[-4:-1]
     with _Call(k.device, stream) as s:
         _check(_lib().spec_kv_append(C.byref(a), s))
+
+
+def tree_attention_workspace_size(Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of workspace tree_attention needs (0 for head layouts it refuses)."""
+    return int(_lib().spec_tree_attention_workspace_size(Hq, Hkv, D))
+
+
+def tree_attention(q, k, v, k_cache, v_cache, block_table, lens, parents, cu_nodes, *,
+                   scale: float | None = None, with_lse: bool = False, out=None, out_lse=None,
+                   workspace=None, stream=None):
+    """Attention of drafted nodes over their sequence's paged context and
+    their own ancestors.  q [N, Hq, D], k, v [N, Hkv, D] (bf16 or fp16): the
+    nodes of all B sequences, packed as cu_nodes [B+1] says; k_cache, v_cache
+    [pages, page_size, Hkv, D]; block_table [B, W], lens [B] (cached tokens),
+    parents [N] int32.  Strides are free but for the last axis.  scale
+    defaults to D ** -0.5.  Returns (out [N, Hq, D], lse [N, Hq] fp32 or
+    None).  `workspace`: a uint8 tensor of tree_attention_workspace_size
+    bytes, of any content; calls that may run at once need one each."""
+    _same_device(q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                 lens=lens, parents=parents, cu_nodes=cu_nodes, out=out, out_lse=out_lse,
+                 workspace=workspace)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
+    _want(q, "q", q.dtype, None, None, None, contiguous=False)
+    N, Hq, D = q.shape
+    _want(k, "k", q.dtype, N, None, D, contiguous=False)
+    Hkv = k.shape[1]
+    _want(v, "v", q.dtype, N, Hkv, D, contiguous=False)
+    _want(k_cache, "k_cache", q.dtype, None, None, Hkv, D, contiguous=False)
+    pages, page = k_cache.shape[:2]
+    _want(v_cache, "v_cache", q.dtype, pages, page, Hkv, D, contiguous=False)
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.stride(-1) != 1 and t.numel() > 0:
+            raise ValueError(f"{n}'s last axis must be contiguous")
+    _want(lens, "lens", torch.int32, None)
+    B = lens.shape[0]
+    _want(cu_nodes, "cu_nodes", torch.int32, B + 1)
+    _want(parents, "parents", torch.int32, N)
+    _want(block_table, "block_table", torch.int32, B, None, contiguous=False)
+    W = block_table.shape[1]
+    if B > 0 and W > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table rows must be contiguous")
+    dev = q.device
+    with _Call(dev, stream) as s:
+        out = _out(out, "out", q.dtype, (N, Hq, D), dev)
+        if with_lse or out_lse is not None:
+            out_lse = _out(out_lse, "out_lse", torch.float32, (N, Hq), dev)
+        if workspace is None:
+            workspace = torch.empty(max(tree_attention_workspace_size(Hq, Hkv, D), 256),
+                                    dtype=torch.uint8, device=dev)
+        a = _AttentionArgs(
+            _p(q), _p(k), _p(v), _p(k_cache), _p(v_cache), _p(out), _p(out_lse),
+            _p(block_table), _p(lens), _p(parents), _p(cu_nodes), *q.stride()[:2],
+            *k.stride()[:2], *v.stride()[:2], *k_cache.stride()[:3], *v_cache.stride()[:3],
+            block_table.stride(0), B, N, Hq, Hkv, D, pages, page, W,
+            1 if q.dtype == torch.bfloat16 else F16, D ** -0.5 if scale is None else scale)
+        _check(_lib().spec_tree_attention(C.byref(a), workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), s))
+    return out, out_lse

@@ -101,3 +101,48 @@ def test_python_checks():
         sv.kv_slots(z, z, z, z[None], z, z[:1], rows=1, page_size=16)
     with pytest.raises(ValueError, match="CUDA"):
         sv.kv_append(t, t, z, t[None], t[None])
+
+
+def test_attention_arguments():
+    L = _tree._lib()
+    assert sv.tree_attention_workspace_size(32, 8, 128) > 0
+    for heads in ((32, 7, 128), (4, 8, 64), (129, 1, 64), (8, 0, 64), (8, 2, 136), (8, 2, 12)):
+        assert sv.tree_attention_workspace_size(*heads) == 0
+
+    def call(ws=FAKE, ws_bytes=1 << 30, **kw):
+        a = _tree._AttentionArgs()
+        for n, t in _tree._AttentionArgs._fields_:
+            if t is ctypes.c_void_p:
+                setattr(a, n, 1 << 20)
+            elif t is ctypes.c_int64:
+                setattr(a, n, 1024)
+        sizes = dict(B=2, N=4, Hq=8, Hkv=2, D=64, num_pages=9, page_size=16, table_width=5,
+                     dtype=1, scale=0.1)
+        for n, x in {**sizes, **kw}.items():
+            setattr(a, n, x)
+        return L.spec_tree_attention(ctypes.byref(a), ws, ws_bytes, None)
+
+    assert call(B=0) == 0 and call(N=0) == 0
+    for kw, status, text in [
+            (dict(dtype=0), 1, b"dtype"), (dict(B=-1), 1, b"B must be"),
+            (dict(N=-1), 1, b"N must be"), (dict(Hkv=3), 1, b"multiple of Hkv"),
+            (dict(Hq=512, Hkv=2), 1, b"multiple of Hkv"), (dict(D=12), 2, b"D must be"),
+            (dict(D=256), 2, b"D must be"), (dict(page_size=24), 2, b"page_size"),
+            (dict(page_size=1), 2, b"page_size"), (dict(page_size=192), 2, b"page_size"),
+            (dict(num_pages=0), 1, b"num_pages"), (dict(table_width=2**28), 1, b"too long"),
+            (dict(scale=0.0), 1, b"scale"), (dict(scale=float("nan")), 1, b"scale"),
+            (dict(scale=float("inf")), 1, b"scale"), (dict(q=None), 1, b"NULL"),
+            (dict(block_table=None), 1, b"NULL"), (dict(v_cache=(1 << 20) + 8), 1, b"16-byte"),
+            (dict(out=(1 << 20) + 2), 1, b"16-byte"), (dict(lens=(1 << 20) + 1), 1, b"aligned"),
+            (dict(q_node=12), 1, b"strides"), (dict(kc_token=0), 1, b"strides"),
+            (dict(vc_page=-8), 1, b"strides"), (dict(ws=None), 4, b"workspace"),
+            (dict(ws=ctypes.c_void_p(64)), 4, b"aligned"), (dict(ws_bytes=100), 4, b"too small")]:
+        _err(call(**kw), status, text)
+    _err(L.spec_tree_attention(None, FAKE, 1 << 30, None), 1, b"NULL")
+
+
+def test_attention_python_checks():
+    x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    z = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        sv.tree_attention(x, x, x, x[None], x[None], z[None], z[:1], z, z)

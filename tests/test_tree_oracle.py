@@ -81,3 +81,19 @@ def test_attention_of_a_hand_case():
                             np.array([3]), np.array([-1, 0, 0]), np.array([0, 3]), 1.0)
     assert np.allclose(out[2, 0], (3 * 9.0 + v[0, 0] + v[2, 0]) / 5)
     assert np.allclose(lse[:, 0], np.log([4, 5, 5]))
+
+
+def test_vectorised_attention_equals_the_plain_one():
+    import torch
+    g = torch.Generator().manual_seed(3)
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g, dtype=torch.float64)
+
+    q, k, v = rnd(7, 4, 8), rnd(7, 2, 8), rnd(7, 2, 8)
+    kc, vc = rnd(5, 4, 2, 8), rnd(5, 4, 2, 8)
+    table = torch.tensor([[3, 1, 0], [4, 2, 0]])
+    lens, par, cu = torch.tensor([9, 3]), torch.tensor([-1, 0, 0, 1, -1, 0, 1]), torch.tensor([0, 4, 7])
+    out, lse, _ = to.attention_t(q, k, v, kc, vc, table, lens, par, cu, 0.3)
+    o2, l2 = to.attention(*(t.numpy() for t in (q, k, v, kc, vc, table, lens, par, cu)), 0.3)
+    assert np.abs(out.numpy() - o2).max() < 1e-12 and np.abs(lse.numpy() - l2).max() < 1e-12

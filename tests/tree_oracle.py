@@ -176,3 +176,47 @@ def attention(q, k, v, k_cache, v_cache, table, lens, parents, cu, scale):
                 out[i, h] = (p[:, None] * V).sum(0) / p.sum()
                 lse[i, h] = m + np.log(p.sum())
     return out, lse
+
+
+def attention_t(q, k, v, k_cache, v_cache, table, lens, parents, cu, scale):
+    """`attention` in torch float64, a sequence at a time on the tensors'
+    device: (out, lse, mean absolute value under the weights)."""
+    import torch
+    N, Hq, D = q.shape
+    Hkv, page = k.shape[1], k_cache.shape[1]
+    G = Hq // Hkv
+    dev = q.device
+    out = torch.zeros(N, Hq, D, dtype=torch.float64, device=dev)
+    mag, lse = torch.zeros_like(out), torch.zeros(N, Hq, dtype=torch.float64, device=dev)
+    cu, lens, par = cu.tolist(), lens.tolist(), parents.tolist()
+    for b, L in enumerate(lens):
+        lo, n = cu[b], cu[b + 1] - cu[b]
+        if n <= 0:
+            continue
+        see = torch.zeros(n, n, dtype=torch.bool)
+        for i in range(n):
+            j = i
+            while j >= 0:
+                see[i, j] = True
+                j = par[lo + j]
+        see = see.to(dev)
+        t = torch.arange(L, device=dev)
+        pg = table[b].long()[t // page]
+        for h in range(Hkv):
+            # what no row of the column sees is cleared; what only some see is masked
+            K = torch.cat([k_cache[pg, t % page, h], k[lo:lo + n, h]]).double()
+            V = torch.cat([v_cache[pg, t % page, h], v[lo:lo + n, h]]).double()
+            Q = q[lo:lo + n, h * G:(h + 1) * G].double()
+            s = torch.einsum("ngd,td->ngt", Q, K) * scale
+            s[:, :, L:] = torch.where(see[:, None], s[:, :, L:], -torch.inf)
+            z = torch.logsumexp(s, -1)
+            p = torch.exp(s - z[..., None])
+            o = torch.einsum("ngt,td->ngd", p, V.nan_to_num(0, 0, 0))
+            for c in torch.nonzero(~V.isfinite().all(1))[:, 0].tolist():  # 0 * inf in masked places
+                w = p[:, :, c, None] * torch.where(V[c].isfinite(), 0.0, V[c])
+                seen = torch.ones(n, dtype=torch.bool, device=dev) if c < L else see[:, c - L]
+                o = o + torch.where(seen[:, None, None], w, 0.0)
+            r = slice(lo, lo + n), slice(h * G, (h + 1) * G)
+            out[r], lse[r] = o, z
+            mag[r] = torch.einsum("ngt,td->ngd", p, V.nan_to_num(0, 0, 0).abs())
+    return out, lse, mag
