@@ -29,6 +29,7 @@
 #include <climits>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "spec_tree.h"
 #include "sv_internal.h"
@@ -40,8 +41,8 @@ namespace {
 constexpr int kTile = 128;          // keys of a tile, rows of a query tile
 constexpr int kWarpsSoft = 8;       // softmax warps: two groups of four
 constexpr int kSoft = 32 * kWarpsSoft;
-constexpr int kWarpKv = 8, kWarpMma = 9, kWarpQ = 10;
-constexpr int kThreads = 32 * 12;     // (the last warp only fills its warpgroup)
+constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpQ = 11;
+constexpr int kThreads = 32 * 12;
 // Registers: the two softmax groups hold a row of 128 scores a thread, the
 // third group needs few.  2 x 208 + 88 = 3 x 168, what a block of 384 threads
 // is launched with.
@@ -139,8 +140,7 @@ struct Shared {
 };
 
 // Wait for a phase; false once any wait of the CTA has run out of time.
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool wait_long(Shared& sh, uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = global_ns();
   for (;;) {
     for (int k = 0; k < 64; ++k)
@@ -152,6 +152,11 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity)
       return false;
     }
   }
+}
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+  for (int k = 0; k < 16; ++k)
+    if (mbar_try_wait(bar, parity)) return true;
+  return wait_long(sh, bar, parity);
 }
 
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -174,6 +179,25 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
   return r;
 }
+// Two fp32 values in one 64-bit register, for the paired instructions.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float pair_lo(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p)); }
+__device__ __forceinline__ float pair_hi(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <bool kBf16>
 constexpr uint32_t kExpMask = kBf16 ? 0x7F80u : 0x7C00u;
 template <bool kBf16>
@@ -280,9 +304,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
   if (warp >= kWarpsSoft) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-  if (warp == kWarpKv) {
+  if (warp == kWarpK || warp == kWarpV) {
     // ---------------------------------------------------- keys and values
-    int t = 0;  // ring position: two stages a tile
+    // one warp each: ring positions 2 t (keys of the CTA's tile t) and 2 t + 1 (its values)
+    const bool kv = warp == kWarpV;
+    const CUtensorMap* own = kv ? &P.vmap : &P.kmap;
+    const CUtensorMap* cached = kv ? &P.vcmap : &P.kcmap;
+    int st = kv ? 1 : 0, ph = 1, t = 0;  // stage, parity of its last release, tiles begun
     bool ok = true;
     while (ok && w.next(P)) {
       const int32_t* row = P.table + w.b * P.table_row;
@@ -293,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         return lane < kTile / P.box && tok < w.s.len ? row[tok / P.page] : 0;
       };
       int page = page_at(w.j0);
-      for (int j = w.j0; ok && j < w.j1; ++j) {
+      for (int j = w.j0; j < w.j1; ++j) {
         const int ahead = page_at(j + 1);
         const bool tree = j < w.s.tt;
         const int first = tree ? (w.s.tt - 1 - j) * kTile : (j - w.s.tt) * kTile;
@@ -301,35 +329,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const int rows = tree ? kTreeBox : P.box;
         const int boxes = cdiv(valid, rows);
         if (page < 0 || page >= P.num_pages) page = 0;  // (the softmax warps mark the rows)
-        const int tok = tree ? 0 : (first + lane * P.box) % P.page;
-        for (int kv = 0; kv < 2; ++kv, ++t) {
-          const int st = t % S::kStages, use = t / S::kStages;
-          if (use > 0 && !__all_sync(0xffffffffu, wait(sh, &sh.empty[st], (use - 1) & 1))) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], boxes * rows * 128 * S::kHalves);
-          __syncwarp();
-          if (lane < boxes) {
-            char* dst = ring + st * S::kTileBytes + lane * rows * 128;
+        ok = __all_sync(0xffffffffu, wait(sh, &sh.empty[st], ph));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], boxes * rows * 128 * S::kHalves);
+        __syncwarp();
+        if (lane < boxes) {
+          char* dst = ring + st * S::kTileBytes + lane * rows * 128;
+          if (tree) {
 #pragma unroll
-            for (int hf = 0; hf < S::kHalves; ++hf) {
-              if (tree) {
-                tma_3d(dst + hf * (kTile * 128), kv ? &P.vmap : &P.kmap, hf * 64, w.h, w.s.lo + first + lane * kTreeBox, &sh.full[st]);
-              } else {
-                tma_4d(dst + hf * (kTile * 128), kv ? &P.vcmap : &P.kcmap, hf * 64, tok, w.h, page, &sh.full[st]);
-              }
-            }
+            for (int hf = 0; hf < S::kHalves; ++hf)
+              tma_3d(dst + hf * (kTile * 128), own, hf * 64, w.h, w.s.lo + first + lane * kTreeBox, &sh.full[st]);
+          } else {
+            const int tok = P.box == kTile ? first % P.page : 0;
+#pragma unroll
+            for (int hf = 0; hf < S::kHalves; ++hf)
+              tma_4d(dst + hf * (kTile * 128), cached, hf * 64, tok, w.h, page, &sh.full[st]);
           }
-          __syncwarp();
         }
+        __syncwarp();
         page = ahead;
+        ++t;
+        if ((st += 2) >= S::kStages) {
+          st -= S::kStages;
+          ph ^= 1;
+        }
       }
     }
     if (!ok) {  // leave no copy in flight behind
       for (int i = max(0, t - S::kStages); i < t; ++i) {
+        const int pos = 2 * i + (kv ? 1 : 0);
         const uint64_t t0 = global_ns();
-        while (!mbar_try_wait(&sh.full[i % S::kStages], (i / S::kStages) & 1) && global_ns() - t0 < kWaitLimitNs) {
+        while (!mbar_try_wait(&sh.full[pos % S::kStages], (pos / S::kStages) & 1) && global_ns() - t0 < kWaitLimitNs) {
         }
       }
     }
@@ -362,64 +392,88 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ----------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t idesc_s = instr_desc(kBf16, kTile, false);
-      const uint32_t idesc_o = instr_desc(kBf16, DP, true);
-      const int ksteps = cdiv(P.D, 16);
-      const uint32_t ring_a = smem_addr(ring), q_a = smem_addr(qtile);
-      int t0 = 0, q0 = 0, seg = 0;
-      int npv[2] = {0, 0};
-      bool ok = true;
-      while (ok && w.next(P)) {
-        const int T = w.j1 - w.j0, steps = w.two ? 2 * T : T;
-        // S of step i, once the tensor memory it goes to is free
-        auto scores = [&](int i) {
-          const int s = i & 1, tile = w.two ? i >> 1 : i;
-          const int kpos = t0 + 2 * tile, st = kpos % S::kStages;
-          const int qpos = q0 + (w.two ? s : 0);
-          if (npv[s] > 0 && !wait(sh, &sh.pvdone[s], (npv[s] - 1) & 1)) return false;
-          if (!wait(sh, &sh.qfull[qpos & 1], (qpos >> 1) & 1)) return false;
-          if (!wait(sh, &sh.full[st], (kpos / S::kStages) & 1)) return false;
-          tc_fence_after();
-          const uint32_t qa = q_a + (qpos & 1) * S::kTileBytes, ka = ring_a + st * S::kTileBytes;
-          for (int k = 0; k < ksteps; ++k) {
-            const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
-            mma_ss(tmem + s * kTile, smem_desc(qa + off, 16), smem_desc(ka + off, 16), idesc_s, k > 0);
+    // (the whole warp keeps the books, one lane issues)
+    const bool issuer = elect_one();
+    constexpr uint32_t idesc_s = instr_desc(kBf16, kTile, false);
+    constexpr uint32_t idesc_o = instr_desc(kBf16, DP, true);
+    constexpr int kStep = S::kTileBytes >> 4;  // from one tile's descriptor to the next's
+    const int ksteps = cdiv(P.D, 16);
+    const uint64_t qdesc = smem_desc(smem_addr(qtile), 16);
+    const uint64_t kdesc = smem_desc(smem_addr(ring), 16);
+    const uint64_t vdesc = smem_desc(smem_addr(ring), kTile * 128);
+    int kst = 0, kph = 0, vst = 1, vph = 0;  // next key and value tile: stage, parity
+    int q0 = 0, seg = 0;                     // query tiles and parts so far
+    uint32_t npv[2] = {0, 0};                // second products so far, by group
+    bool ok = true;
+    while (ok && w.next(P)) {
+      const int T = w.j1 - w.j0;
+      const bool two = w.two;
+      const int steps = two ? 2 * T : T;
+      // S of group s from the next key tile, once the tensor memory it goes to is free;
+      // `last`: the group's last of this part
+      auto scores = [&](int s, bool last) {
+        const int qs = (q0 + (two ? s : 0)) & 1;
+        bool fine = npv[s] == 0 || wait(sh, &sh.pvdone[s], (npv[s] - 1) & 1);
+        fine = fine && ((two && s) || wait(sh, &sh.full[kst], kph));
+        if (!__all_sync(0xffffffffu, fine)) return false;
+        tc_fence_after();
+        if (issuer) {
+          const uint64_t da = qdesc + qs * kStep, db = kdesc + kst * kStep;
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const int off = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
+            if (k < ksteps) mma_ss(tmem + s * kTile, da + off, db + off, idesc_s, k > 0);
           }
           mma_commit(&sh.sfull[s]);
-          if (!w.two || s == 1) mma_commit(&sh.empty[st]);
-          if (tile == T - 1) mma_commit(&sh.qempty[qpos & 1]);
-          return true;
-        };
-        ok = scores(0) && (steps < 2 || scores(1));
-        for (int i = 0; ok && i < steps; ++i) {
-          const int s = i & 1, tile = w.two ? i >> 1 : i;
-          const int vpos = t0 + 2 * tile + 1, st = vpos % S::kStages;
-          if (i == 0 && seg > 0 && !wait(sh, &sh.oempty, (seg - 1) & 1)) {
-            ok = false;
-            break;
+          if (!two || s) mma_commit(&sh.empty[kst]);
+          if (last) mma_commit(&sh.qempty[qs]);
+        }
+        __syncwarp();
+        if (!two || s) {
+          if ((kst += 2) >= S::kStages) {
+            kst -= S::kStages;
+            kph ^= 1;
           }
-          ok = wait(sh, &sh.full[st], (vpos / S::kStages) & 1) && wait(sh, &sh.pready[s], npv[s] & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t va = ring_a + st * S::kTileBytes;
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + k * 8,
-                   smem_desc(va + k * 2048, kTile * 128), idesc_o, i >= 2 || k > 0);
+        }
+        return true;
+      };
+      ok = wait(sh, &sh.qfull[q0 & 1], (q0 >> 1) & 1);
+      if (two) ok = ok && wait(sh, &sh.qfull[(q0 + 1) & 1], ((q0 + 1) >> 1) & 1);
+      ok = __all_sync(0xffffffffu, ok) && scores(0, T == 1) && (steps < 2 || scores(1, two ? T == 1 : T == 2));
+      if (ok && seg > 0) ok = __all_sync(0xffffffffu, wait(sh, &sh.oempty, (seg - 1) & 1));
+      for (int i = 0; ok && i < steps; ++i) {
+        const int s = i & 1;
+        bool fine = (two && s) || wait(sh, &sh.full[vst], vph);
+        fine = fine && wait(sh, &sh.pready[s], npv[s] & 1);
+        ok = __all_sync(0xffffffffu, fine);
+        if (!ok) break;
+        tc_fence_after();
+        if (issuer) {
+          const uint32_t o = tmem + 2 * kTile + s * kTile, p = tmem + s * kTile;
+          const uint64_t db = vdesc + vst * kStep;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k) mma_ts(o, p + k * 8, db + k * (2048 >> 4), idesc_o, k > 0 || i >= 2);
           mma_commit(&sh.pvdone[s]);
-          if (!w.two || s == 1) mma_commit(&sh.empty[st]);
-          ++npv[s];
-          if (i + 2 < steps) ok = scores(i + 2);
+          if (!two || s) mma_commit(&sh.empty[vst]);
         }
-        t0 += 2 * T;
-        q0 += w.two ? 2 : 1;
-        ++seg;
+        __syncwarp();
+        if (!two || s) {
+          if ((vst += 2) >= S::kStages) {
+            vst -= S::kStages;
+            vph ^= 1;
+          }
+        }
+        if (s) ++npv[1]; else ++npv[0];
+        // the last key tile's query tiles are free after it (with one query tile: after step T - 1)
+        if (i + 2 < steps) ok = scores(s, two ? i + 4 >= steps : i + 3 == steps);
       }
-      if (!ok) {  // let the products in flight end
-        mma_commit(&sh.drain);
-        const uint64_t ts = global_ns();
-        while (!mbar_try_wait(&sh.drain, 0) && global_ns() - ts < kWaitLimitNs) {
-        }
+      q0 += two ? 2 : 1;
+      ++seg;
+    }
+    if (!ok) {  // let the products in flight end
+      if (issuer) mma_commit(&sh.drain);
+      const uint64_t ts = global_ns();
+      while (!mbar_try_wait(&sh.drain, 0) && global_ns() - ts < kWaitLimitNs) {
       }
     }
     __syncwarp();
@@ -432,9 +486,71 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + wg * kTile, o_at = tmem + lanes + 2 * kTile;
     const float sl = P.sl;
-    int t0 = 0, steps_done = 0;  // ring position; steps of this group so far
+    int t0 = 0;                 // ring position
+    uint32_t steps_done = 0;    // steps of this group so far
     bool alive = true;
     int dseg = 0;
+    float shift = 0.0f, sum = 0.0f;  // this row's exponent shift (base 2) and sum of weights
+
+    // S of one key tile to P: shift, sum and, when a maximum has grown much, the accumulator.
+    // kMask: 0 every key counts, 1 the first `valid`, 2 those in `see`.
+    auto weigh = [&](auto mask, bool fresh, bool mine, int valid, const uint32_t* see) {
+      constexpr int kMask = decltype(mask)::value;
+      float x[kTile];
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) tmem_ld32(s_at + c, x + c);
+      tc_wait_ld();
+      if constexpr (kMask == 2) {
+#pragma unroll
+        for (int c = 0; c < kTile; ++c)
+          if (!(see[c >> 5] >> (c & 31) & 1)) x[c] = -INFINITY;
+      } else if constexpr (kMask == 1) {
+#pragma unroll
+        for (int c = 0; c < kTile; ++c)
+          if (c >= valid) x[c] = -INFINITY;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < kTile; c += 2) mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], x[c]), x[c + 1]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+      if (fresh) {
+        shift = top;
+      } else if (__any_sync(0xffffffffu, mine && top - shift > kGrow)) {
+        const float now = fmaxf(shift, top);
+        const float f = now == shift ? 1.0f : ex2_approx(shift - now);
+        shift = now;
+        sum *= f;
+#pragma unroll 1
+        for (int c = 0; c < DP; c += 16) {
+          float o[16];
+          tmem_ld16(o_at + wg * kTile + c, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] *= f;
+          tmem_st16(o_at + wg * kTile + c, reinterpret_cast<uint32_t*>(o));
+        }
+      }
+      const float neg = shift == -INFINITY ? 0.0f : -shift;
+      const uint64_t sl2 = pair(sl, sl), neg2 = pair(neg, neg);
+      uint64_t part[2] = {0, 0};
+#pragma unroll
+      for (int c0 = 0; c0 < kTile; c0 += 32) {
+        // weights rounded to the input type (relative 2^-8 / 2^-11 at most, as the output
+        // itself is, and averaged over the keys); the sum takes them unrounded
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const uint64_t y = fma2(pair(x[c0 + c], x[c0 + c + 1]), sl2, neg2);
+          const float a = ex2_approx(pair_lo(y)), b = ex2_approx(pair_hi(y));
+          part[(c >> 1) & 1] = add2(part[(c >> 1) & 1], pair(a, b));
+          pk[c >> 1] = pack2<kBf16>(a, b);
+        }
+        tmem_st16(s_at + (c0 >> 1), pk);
+      }
+      const uint64_t p = add2(part[0], part[1]);
+      sum += pair_lo(p) + pair_hi(p);
+      tc_wait_st();
+    };
     while (w.next(P)) {
       const int T = w.j1 - w.j0;
       const int node = w.u * 2 * P.npt + (w.two ? wg * P.npt : 0) + rnode;  // within the sequence
@@ -453,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       }
       if (tid == 0) sh.badv = 0;
       bad = soft_sync_or(bad);
-      float shift = -INFINITY, sum = 0.0f;
+      shift = -INFINITY;
+      sum = 0.0f;
       int up = mine ? node : -1;  // next ancestor to pass
       const int mysteps = w.two ? T : (T + 1 - wg) / 2;
       for (int i = 0; i < mysteps; ++i) {
@@ -514,59 +631,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         ++steps_done;
         if (alive && busy) {
           tc_fence_after();
-          float x[kTile];
-#pragma unroll
-          for (int c = 0; c < kTile; c += 32) tmem_ld32(s_at + c, x + c);
-          tc_wait_ld();
           if (tree) {
-#pragma unroll
-            for (int c = 0; c < kTile; ++c)
-              if (!(see[c >> 5] >> (c & 31) & 1)) x[c] = -INFINITY;
+            weigh(std::integral_constant<int, 2>(), i == 0, mine, valid, see);
           } else if (valid < kTile) {
-#pragma unroll
-            for (int c = 0; c < kTile; ++c)
-              if (c >= valid) x[c] = -INFINITY;
+            weigh(std::integral_constant<int, 1>(), i == 0, mine, valid, nullptr);
+          } else {
+            weigh(std::integral_constant<int, 0>(), i == 0, mine, valid, nullptr);
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
-          if (i == 0) {
-            shift = top;
-          } else if (__any_sync(0xffffffffu, mine && top - shift > kGrow)) {
-            const float now = fmaxf(shift, top);
-            const float f = now == shift ? 1.0f : ex2_approx(shift - now);
-            shift = now;
-            sum *= f;
-#pragma unroll 1
-            for (int c = 0; c < DP; c += 16) {
-              float o[16];
-              tmem_ld16(o_at + wg * kTile + c, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] *= f;
-              tmem_st16(o_at + wg * kTile + c, reinterpret_cast<uint32_t*>(o));
-            }
-          }
-          const float neg = shift == -INFINITY ? 0.0f : -shift;
-          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int c0 = 0; c0 < kTile; c0 += 32) {
-            // weights rounded to the input type (relative 2^-8 / 2^-11 at most, as the output
-            // itself is, and averaged over the keys); the sum takes them unrounded
-            uint32_t pk[16];
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float a = ex2_approx(fmaf(x[c0 + c], sl, neg));
-              const float b = ex2_approx(fmaf(x[c0 + c + 1], sl, neg));
-              part[c & 3] += a;
-              part[(c + 1) & 3] += b;
-              pk[c >> 1] = pack2<kBf16>(a, b);
-            }
-            tmem_st16(s_at + (c0 >> 1), pk);
-          }
-          sum += (part[0] + part[1]) + (part[2] + part[3]);
-          tc_wait_st();
           tc_fence_before();
         }
         mbar_arrive(&sh.pready[wg]);
