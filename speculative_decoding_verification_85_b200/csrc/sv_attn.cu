@@ -40,8 +40,7 @@ namespace {
 
 constexpr int kTile = 128;          // keys of a tile, rows of a query tile
 constexpr int kWarpsSoft = 8;       // softmax warps: two groups of four
-constexpr int kSoft = 32 * kWarpsSoft;
-constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpQ = 11;
+constexpr int kWarpV = 9, kWarpMma = 10;  // 8: keys, 9: values, 10 and 11: products of each softmax group
 constexpr int kThreads = 32 * 12;
 // Registers: the two softmax groups hold a row of 128 scores a thread, the
 // third group needs few.  2 x 208 + 88 = 3 x 168, what a block of 384 threads
@@ -51,12 +50,21 @@ constexpr float kGrow = 8.0f;       // base-2 growth of a maximum that is let st
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTreeBox = 16;        // rows of one load of the nodes' own keys and values
 
+// Ring of key and value tiles.  Tile t of the CTA goes to pair t % kPairs: its
+// keys to stage 2 (t % kPairs), its values to the next one, lap t / kPairs.
+// With one query tile group t % 2 takes tile t, with two query tiles both do.
+// The number of pairs is even, so in either mode a group passes every lap of
+// the pairs of its own parity; it passes all laps of the others once both
+// groups have met at the start of a part with two query tiles.  A barrier's
+// parity therefore never stands for a lap that a waiter has not seen.
 template <int DP>
 struct Shape {
   static constexpr int kHalves = DP / 64;
   static constexpr int kTileBytes = kTile * DP * 2;
-  static constexpr int kStages = DP == 128 ? 5 : 10;
-  static constexpr size_t kTiles = static_cast<size_t>(2 + kStages) * kTileBytes;
+  static constexpr int kPairs = DP == 128 ? 2 : 4;
+  static constexpr size_t kTiles = static_cast<size_t>(2 + 2 * kPairs) * kTileBytes;
+  static __device__ __forceinline__ int stage(int t) { return 2 * (t % kPairs); }
+  static __device__ __forceinline__ uint32_t parity(int t) { return (t / kPairs) & 1; }
 };
 
 struct alignas(64) AttnParams {
@@ -69,6 +77,7 @@ struct alignas(64) AttnParams {
   int B, N, Hq, Hkv, G, D, num_pages, page, width;
   int box;             // tokens of one load from a page
   int npt;             // nodes of one query tile
+  int ctas;
   float sl;            // scale * log2(e)
   float* part_o;       // partial results: [cta][2][tile][DP / 4][128][4]
   float2* part_s;      // [cta][2][tile][128] (shift, sum)
@@ -83,14 +92,13 @@ struct Seq {
   bool mark;
 };
 __device__ __forceinline__ Seq seq_of(const AttnParams& P, int b) {
+  const int lo = P.cu[b], hi = P.cu[b + 1], len = P.lens[b];
   Seq s{};
-  s.lo = P.cu[b];
-  const int hi = P.cu[b + 1];
-  if (s.lo < 0 || hi > P.N || hi <= s.lo) return s;
-  s.n = hi - s.lo;
-  s.len = P.lens[b];
-  s.mark = s.n > SV_MAX_NODES || s.len < 0 || s.len > static_cast<int64_t>(P.width) * P.page;
-  if (s.mark) s.len = 0;
+  if (lo < 0 || hi > P.N || hi <= lo) return s;
+  s.lo = lo;
+  s.n = hi - lo;
+  s.mark = s.n > SV_MAX_NODES || len < 0 || len > static_cast<int64_t>(P.width) * P.page;
+  s.len = s.mark ? 0 : len;
   s.tt = cdiv(min(s.n, SV_MAX_NODES), kTile);
   s.J = s.tt + cdiv(s.len, kTile);
   s.U = cdiv(s.n, 2 * P.npt);
@@ -130,13 +138,15 @@ struct Walk {
 };
 
 struct Shared {
-  uint64_t full[10], empty[10];
-  uint64_t qfull[2], qempty[2], sfull[2], pready[2], pvdone[2], oempty, drain;
-  float2 xch[2][kTile];
+  uint64_t full[8], empty[8];
+  uint64_t qfull[2], sfull[2], pready[2], pvdone[2], oempty[2], drain[2], meet;
+  float2 xch[2][kTile];       // [group][row]: shift, sum
   int64_t scan[16];
   Walk start;
   uint32_t tmem;
-  int dead, badv;
+  int dead;
+  int badv[4];                // [part & 3]: a tree tile holds infinities or NaN among its values
+  int badpage[8];             // [part & 7]: a page outside the cache
 };
 
 // Wait for a phase; false once any wait of the CTA has run out of time.
@@ -160,14 +170,6 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity)
 }
 
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ bool soft_sync_or(bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r) : "r"(static_cast<uint32_t>(x)) : "memory");
-  return r != 0;
-}
 
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -223,22 +225,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   const int cta = blockIdx.x;
 
   if (tid == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
+    for (int i = 0; i < 2 * S::kPairs; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.empty[i], 2);  // both groups' products
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.qfull[i], 1);
-      mbar_init(&sh.qempty[i], 1);
       mbar_init(&sh.sfull[i], 1);
       mbar_init(&sh.pready[i], kTile);
       mbar_init(&sh.pvdone[i], 1);
+      mbar_init(&sh.oempty[i], kWarpsSoft);
+      mbar_init(&sh.drain[i], 1);
     }
-    mbar_init(&sh.oempty, kWarpsSoft);
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.meet, 2);
+    for (int i = 0; i < 4; ++i) sh.badv[i] = 0;
     mbar_init_fence();
     sh.dead = 0;
-    sh.badv = 0;
+  }
+  if (tid >= 32 && tid < 37) {  // the maps, while the stretch is worked out
+    const CUtensorMap* maps = &P.qmap;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(maps + (tid - 32)) : "memory");
   }
   if (warp == kWarpMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
@@ -303,181 +309,176 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   const uint32_t tmem = sh.tmem;
 
   if (warp >= kWarpsSoft) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-  if (warp == kWarpK || warp == kWarpV) {
-    // ---------------------------------------------------- keys and values
-    // one warp each: ring positions 2 t (keys of the CTA's tile t) and 2 t + 1 (its values)
-    const bool kv = warp == kWarpV;
-    const CUtensorMap* own = kv ? &P.vmap : &P.kmap;
-    const CUtensorMap* cached = kv ? &P.vcmap : &P.kcmap;
-    int st = kv ? 1 : 0, ph = 1, t = 0;  // stage, parity of its last release, tiles begun
-    bool ok = true;
-    while (ok && w.next(P)) {
-      const int32_t* row = P.table + w.b * P.table_row;
-      // this lane's page of the next context tile, read a tile ahead
-      auto page_at = [&](int j) {
-        if (j < w.s.tt || j >= w.j1) return 0;
-        const int tok = (j - w.s.tt) * kTile + lane * P.box;
-        return lane < kTile / P.box && tok < w.s.len ? row[tok / P.page] : 0;
-      };
-      int page = page_at(w.j0);
-      for (int j = w.j0; j < w.j1; ++j) {
-        const int ahead = page_at(j + 1);
-        const bool tree = j < w.s.tt;
-        const int first = tree ? (w.s.tt - 1 - j) * kTile : (j - w.s.tt) * kTile;
-        const int valid = min(kTile, (tree ? min(w.s.n, SV_MAX_NODES) : w.s.len) - first);
-        const int rows = tree ? kTreeBox : P.box;
-        const int boxes = cdiv(valid, rows);
-        if (page < 0 || page >= P.num_pages) page = 0;  // (the softmax warps mark the rows)
-        ok = __all_sync(0xffffffffu, wait(sh, &sh.empty[st], ph));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], boxes * rows * 128 * S::kHalves);
-        __syncwarp();
-        if (lane < boxes) {
-          char* dst = ring + st * S::kTileBytes + lane * rows * 128;
-          if (tree) {
-#pragma unroll
-            for (int hf = 0; hf < S::kHalves; ++hf)
-              tma_3d(dst + hf * (kTile * 128), own, hf * 64, w.h, w.s.lo + first + lane * kTreeBox, &sh.full[st]);
-          } else {
-            const int tok = P.box == kTile ? first % P.page : 0;
-#pragma unroll
-            for (int hf = 0; hf < S::kHalves; ++hf)
-              tma_4d(dst + hf * (kTile * 128), cached, hf * 64, tok, w.h, page, &sh.full[st]);
-          }
-        }
-        __syncwarp();
-        page = ahead;
-        ++t;
-        if ((st += 2) >= S::kStages) {
-          st -= S::kStages;
-          ph ^= 1;
-        }
-      }
-    }
-    if (!ok) {  // leave no copy in flight behind
-      for (int i = max(0, t - S::kStages); i < t; ++i) {
-        const int pos = 2 * i + (kv ? 1 : 0);
-        const uint64_t t0 = global_ns();
-        while (!mbar_try_wait(&sh.full[pos % S::kStages], (pos / S::kStages) & 1) && global_ns() - t0 < kWaitLimitNs) {
-        }
-      }
-    }
-  } else if (warp == kWarpQ) {
-    // ------------------------------------------------------------ queries
-    if (lane == 0) {
-      int q = 0;  // query tiles loaded
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp < kWarpMma) {
+      // -------------------------------------------------- keys and values
+      // one warp each
+      const bool kv = warp == kWarpV;
+      const CUtensorMap* own = kv ? &P.vmap : &P.kmap;
+      const CUtensorMap* cached = kv ? &P.vcmap : &P.kcmap;
+      int t = 0, seg = 0;
       bool ok = true;
       while (ok && w.next(P)) {
-        for (int i = 0; ok && i < (w.two ? 2 : 1); ++i, ++q) {
-          const int st = q & 1, use = q >> 1;
-          if (use > 0 && !wait(sh, &sh.qempty[st], (use - 1) & 1)) {
-            ok = false;
-            break;
+        const int32_t* row = P.table + w.b * P.table_row;
+        // this lane's page of a context tile (read a tile ahead): its load's page where pages
+        // are smaller than a tile, else the tile's
+        const int per = kTile / P.box, span = P.page / P.box;
+        auto page_at = [&](int j) {
+          const int c = j - w.s.tt;
+          if (c < 0 || j >= w.j1 || lane >= per || c * kTile + lane * P.box >= w.s.len) return 0;
+          return row[span == 1 ? c * per + lane : c / span];
+        };
+        int page = page_at(w.j0);
+        if (!kv && lane == 0) sh.badpage[seg & 7] = 0;
+        __syncwarp();
+        for (int j = w.j0; j < w.j1; ++j) {
+          const int ahead = page_at(j + 1);
+          const bool tree = j < w.s.tt;
+          const int c = tree ? w.s.tt - 1 - j : j - w.s.tt;  // tile of the tree, of the context
+          const int valid = min(kTile, (tree ? min(w.s.n, SV_MAX_NODES) : w.s.len) - c * kTile);
+          const int rows = tree ? kTreeBox : P.box;
+          const int boxes = (valid + rows - 1) / rows;
+          if (page < 0 || page >= P.num_pages) {
+            if (!kv) sh.badpage[seg & 7] = 1;  // the rows will be marked
+            page = 0;
           }
-          mbar_arrive_expect_tx(&sh.qfull[st], P.npt * P.G * 128 * S::kHalves);
-          for (int hf = 0; hf < S::kHalves; ++hf)
-            tma_3d(qtile + st * S::kTileBytes + hf * (kTile * 128), &P.qmap, hf * 64, w.h * P.G,
-                   w.s.lo + (w.u * 2 + i) * P.npt, &sh.qfull[st]);
+          const int st = S::stage(t) + (kv ? 1 : 0);
+          ok = __all_sync(0xffffffffu, wait(sh, &sh.empty[st], S::parity(t) ^ 1));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], boxes * rows * 128 * S::kHalves);
+          __syncwarp();
+          if (lane < boxes) {
+            char* dst = ring + st * S::kTileBytes + lane * rows * 128;
+            if (tree) {
+#pragma unroll
+              for (int hf = 0; hf < S::kHalves; ++hf)
+                tma_3d(dst + hf * (kTile * 128), own, hf * 64, w.h, w.s.lo + c * kTile + lane * kTreeBox, &sh.full[st]);
+            } else {
+              const int tok = span == 1 ? 0 : (c % span) * kTile;
+#pragma unroll
+              for (int hf = 0; hf < S::kHalves; ++hf)
+                tma_4d(dst + hf * (kTile * 128), cached, hf * 64, tok, w.h, page, &sh.full[st]);
+            }
+          }
+          __syncwarp();
+          page = ahead;
+          ++t;
         }
+        ++seg;
       }
-      if (!ok) {
-        for (int i = max(0, q - 2); i < q; ++i) {
+      if (!ok) {  // leave no copy in flight behind
+        for (int i = max(0, t - S::kPairs); i < t; ++i) {
           const uint64_t t0 = global_ns();
-          while (!mbar_try_wait(&sh.qfull[i & 1], (i >> 1) & 1) && global_ns() - t0 < kWaitLimitNs) {
+          while (!mbar_try_wait(&sh.full[S::stage(i) + (kv ? 1 : 0)], S::parity(i)) && global_ns() - t0 < kWaitLimitNs) {
           }
         }
       }
-    }
-    __syncwarp();
-  } else if (warp == kWarpMma) {
-    // ----------------------------------------------------------- products
-    // (the whole warp keeps the books, one lane issues)
-    const bool issuer = elect_one();
-    constexpr uint32_t idesc_s = instr_desc(kBf16, kTile, false);
-    constexpr uint32_t idesc_o = instr_desc(kBf16, DP, true);
-    constexpr int kStep = S::kTileBytes >> 4;  // from one tile's descriptor to the next's
-    const int ksteps = cdiv(P.D, 16);
-    const uint64_t qdesc = smem_desc(smem_addr(qtile), 16);
-    const uint64_t kdesc = smem_desc(smem_addr(ring), 16);
-    const uint64_t vdesc = smem_desc(smem_addr(ring), kTile * 128);
-    int kst = 0, kph = 0, vst = 1, vph = 0;  // next key and value tile: stage, parity
-    int q0 = 0, seg = 0;                     // query tiles and parts so far
-    uint32_t npv[2] = {0, 0};                // second products so far, by group
-    bool ok = true;
-    while (ok && w.next(P)) {
-      const int T = w.j1 - w.j0;
-      const bool two = w.two;
-      const int steps = two ? 2 * T : T;
-      // S of group s from the next key tile, once the tensor memory it goes to is free;
-      // `last`: the group's last of this part
-      auto scores = [&](int s, bool last) {
-        const int qs = (q0 + (two ? s : 0)) & 1;
-        bool fine = npv[s] == 0 || wait(sh, &sh.pvdone[s], (npv[s] - 1) & 1);
-        fine = fine && ((two && s) || wait(sh, &sh.full[kst], kph));
-        if (!__all_sync(0xffffffffu, fine)) return false;
-        tc_fence_after();
-        if (issuer) {
-          const uint64_t da = qdesc + qs * kStep, db = kdesc + kst * kStep;
-#pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const int off = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
-            if (k < ksteps) mma_ss(tmem + s * kTile, da + off, db + off, idesc_s, k > 0);
-          }
-          mma_commit(&sh.sfull[s]);
-          if (!two || s) mma_commit(&sh.empty[kst]);
-          if (last) mma_commit(&sh.qempty[qs]);
-        }
-        __syncwarp();
-        if (!two || s) {
-          if ((kst += 2) >= S::kStages) {
-            kst -= S::kStages;
-            kph ^= 1;
-          }
-        }
-        return true;
+      __syncwarp();
+    } else {
+      // --------------------------------------------------------- products
+      // one warp for each softmax group, with the group's own copy of its query tile; the whole
+      // warp keeps the books, one lane issues
+      const int s = warp - kWarpMma;
+      const bool issuer = elect_one();
+      constexpr uint32_t idesc_s = instr_desc(kBf16, kTile, false);
+      constexpr uint32_t idesc_o = instr_desc(kBf16, DP, true);
+      constexpr int kStep = S::kTileBytes >> 4;  // from one tile's descriptor to the next's
+      const int ksteps = cdiv(P.D, 16);
+      const uint64_t qdesc = smem_desc(smem_addr(qtile) + s * S::kTileBytes, 16);
+      const uint64_t kdesc = smem_desc(smem_addr(ring), 16);
+      const uint64_t vdesc = smem_desc(smem_addr(ring), kTile * 128);
+      const uint32_t s_at = tmem + s * kTile, o_at = tmem + 2 * kTile + s * kTile;
+      int t0 = 0;  // tiles so far
+      // second products, query tiles loaded, parts with steps, parts with two query tiles so far
+      uint32_t npv = 0, nq = 0, nown = 0, ntwo = 0;
+      // steps of this group in the part that begins at tile t
+      auto steps_of = [&](const Walk& x, int t) {
+        const int T = x.j1 - x.j0;
+        return x.two ? T : (T + 1 - ((s ^ t) & 1)) / 2;
       };
-      ok = wait(sh, &sh.qfull[q0 & 1], (q0 >> 1) & 1);
-      if (two) ok = ok && wait(sh, &sh.qfull[(q0 + 1) & 1], ((q0 + 1) >> 1) & 1);
-      ok = __all_sync(0xffffffffu, ok) && scores(0, T == 1) && (steps < 2 || scores(1, two ? T == 1 : T == 2));
-      if (ok && seg > 0) ok = __all_sync(0xffffffffu, wait(sh, &sh.oempty, (seg - 1) & 1));
-      for (int i = 0; ok && i < steps; ++i) {
-        const int s = i & 1;
-        bool fine = (two && s) || wait(sh, &sh.full[vst], vph);
-        fine = fine && wait(sh, &sh.pready[s], npv[s] & 1);
-        ok = __all_sync(0xffffffffu, fine);
-        if (!ok) break;
-        tc_fence_after();
+      auto load_q = [&](const Walk& x) {
         if (issuer) {
-          const uint32_t o = tmem + 2 * kTile + s * kTile, p = tmem + s * kTile;
-          const uint64_t db = vdesc + vst * kStep;
+          mbar_arrive_expect_tx(&sh.qfull[s], P.npt * P.G * 128 * S::kHalves);
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) mma_ts(o, p + k * 8, db + k * (2048 >> 4), idesc_o, k > 0 || i >= 2);
-          mma_commit(&sh.pvdone[s]);
-          if (!two || s) mma_commit(&sh.empty[vst]);
+          for (int hf = 0; hf < S::kHalves; ++hf)
+            tma_3d(qtile + s * S::kTileBytes + hf * (kTile * 128), &P.qmap, hf * 64, x.h * P.G,
+                   x.s.lo + (x.u * 2 + (x.two ? s : 0)) * P.npt, &sh.qfull[s]);
         }
         __syncwarp();
-        if (!two || s) {
-          if ((vst += 2) >= S::kStages) {
-            vst -= S::kStages;
-            vph ^= 1;
+        ++nq;
+      };
+      bool ok = true;
+      bool more = w.next(P);
+      if (more && steps_of(w, 0)) load_q(w);
+      while (ok && more) {
+        const bool two = w.two;
+        const int steps = steps_of(w, t0), stride = two ? 1 : 2;
+        int t = two ? t0 : t0 + ((s ^ t0) & 1);  // own tile
+        t0 += w.j1 - w.j0;
+        more = w.next(P);
+        auto scores = [&]() {  // S of tile t
+          const int st = S::stage(t);
+          if (!__all_sync(0xffffffffu, wait(sh, &sh.full[st], S::parity(t)))) return false;
+          tc_fence_after();
+          if (issuer) {
+            const uint64_t db = kdesc + st * kStep;
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+              const int off = ((i >> 2) * (kTile * 128) + (i & 3) * 32) >> 4;
+              if (i < ksteps) mma_ss(s_at, qdesc + off, db + off, idesc_s, i > 0);
+            }
+            mma_commit(&sh.sfull[s]);
+            mma_commit(&sh.empty[st]);
+            if (!two) mma_commit(&sh.empty[st]);  // (the other group's share)
           }
+          __syncwarp();
+          return true;
+        };
+        if (two) {  // the other group has passed all tiles before this part, too
+          if (issuer) mbar_arrive(&sh.meet);
+          ok = __all_sync(0xffffffffu, wait(sh, &sh.meet, ntwo & 1));
+          if (!ok) break;
+          ++ntwo;
         }
-        if (s) ++npv[1]; else ++npv[0];
-        // the last key tile's query tiles are free after it (with one query tile: after step T - 1)
-        if (i + 2 < steps) ok = scores(s, two ? i + 4 >= steps : i + 3 == steps);
+        if (steps > 0) {
+          ok = (npv == 0 || wait(sh, &sh.pvdone[s], (npv - 1) & 1)) && wait(sh, &sh.qfull[s], (nq - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok) && scores();
+          if (ok && nown > 0) ok = __all_sync(0xffffffffu, wait(sh, &sh.oempty[s], (nown - 1) & 1));
+          ++nown;
+        }
+        for (int i = 0; ok && i < steps; ++i) {
+          const int st = S::stage(t) + 1;
+          ok = wait(sh, &sh.full[st], S::parity(t)) && wait(sh, &sh.pready[s], npv & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (issuer) {
+            const uint64_t db = vdesc + st * kStep;
+#pragma unroll
+            for (int q = 0; q < kTile / 16; ++q) mma_ts(o_at, s_at + q * 8, db + q * (2048 >> 4), idesc_o, q > 0 || i > 0);
+            mma_commit(&sh.pvdone[s]);
+            mma_commit(&sh.empty[st]);
+            if (!two) mma_commit(&sh.empty[st]);
+          }
+          __syncwarp();
+          t += stride;
+          ++npv;
+          // the next S takes the place of the weights just used
+          if (i + 1 < steps) ok = __all_sync(0xffffffffu, wait(sh, &sh.pvdone[s], (npv - 1) & 1)) && scores();
+        }
+        // the part's last S is done: its query tile can go
+        if (ok && more && steps_of(w, t0)) load_q(w);
       }
-      q0 += two ? 2 : 1;
-      ++seg;
-    }
-    if (!ok) {  // let the products in flight end
-      if (issuer) mma_commit(&sh.drain);
-      const uint64_t ts = global_ns();
-      while (!mbar_try_wait(&sh.drain, 0) && global_ns() - ts < kWaitLimitNs) {
+      if (!ok) {  // let the products and the copy in flight end
+        if (issuer) mma_commit(&sh.drain[s]);
+        const uint64_t ts = global_ns();
+        while (!mbar_try_wait(&sh.drain[s], 0) && global_ns() - ts < kWaitLimitNs) {
+        }
+        while (nq > 0 && !mbar_try_wait(&sh.qfull[s], (nq - 1) & 1) && global_ns() - ts < kWaitLimitNs) {
+        }
       }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
@@ -486,28 +487,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + wg * kTile, o_at = tmem + lanes + 2 * kTile;
     const float sl = P.sl;
-    int t0 = 0;                 // ring position
+    int t0 = 0, dseg = 0;       // tiles and parts so far
     uint32_t steps_done = 0;    // steps of this group so far
     bool alive = true;
-    int dseg = 0;
     float shift = 0.0f, sum = 0.0f;  // this row's exponent shift (base 2) and sum of weights
 
     // S of one key tile to P: shift, sum and, when a maximum has grown much, the accumulator.
-    // kMask: 0 every key counts, 1 the first `valid`, 2 those in `see`.
-    auto weigh = [&](auto mask, bool fresh, bool mine, int valid, const uint32_t* see) {
-      constexpr int kMask = decltype(mask)::value;
+    // kMasked: only the keys in `see` count.
+    auto weigh = [&](auto masked, bool fresh, bool mine, const uint32_t* see) {
       float x[kTile];
 #pragma unroll
       for (int c = 0; c < kTile; c += 32) tmem_ld32(s_at + c, x + c);
       tc_wait_ld();
-      if constexpr (kMask == 2) {
+      if constexpr (decltype(masked)::value) {
 #pragma unroll
         for (int c = 0; c < kTile; ++c)
           if (!(see[c >> 5] >> (c & 31) & 1)) x[c] = -INFINITY;
-      } else if constexpr (kMask == 1) {
-#pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          if (c >= valid) x[c] = -INFINITY;
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -551,116 +546,123 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       sum += pair_lo(p) + pair_hi(p);
       tc_wait_st();
     };
+
     while (w.next(P)) {
-      const int T = w.j1 - w.j0;
+      const int T = w.j1 - w.j0, buf = dseg & 3;
       const int node = w.u * 2 * P.npt + (w.two ? wg * P.npt : 0) + rnode;  // within the sequence
       const bool mine = rnode < P.npt && node < w.s.n;
       const bool busy = __any_sync(0xffffffffu, mine);  // does this warp hold a row at all
       const int32_t* parents = P.parents + w.s.lo;
-      // pages outside the cache: this part's rows are marked
       bool bad = w.s.mark;
-      if (w.j1 > w.s.tt) {
-        const int c0 = max(w.j0 - w.s.tt, 0) * kTile, c1 = min(w.s.len, (w.j1 - w.s.tt) * kTile);
-        const int32_t* row = P.table + w.b * P.table_row;
-        for (int p = c0 / P.page + tid; p <= (c1 - 1) / P.page; p += kSoft) {
-          const int id = row[p];
-          bad |= id < 0 || id >= P.num_pages;
-        }
-      }
-      if (tid == 0) sh.badv = 0;
-      bad = soft_sync_or(bad);
       shift = -INFINITY;
       sum = 0.0f;
       int up = mine ? node : -1;  // next ancestor to pass
-      const int mysteps = w.two ? T : (T + 1 - wg) / 2;
+      // the groups' steps in this part (with one query tile tile t is group t % 2's)
+      const int steps0 = w.two ? T : (T + 1 - (t0 & 1)) / 2, steps1 = w.two ? T : T - steps0;
+      const int mysteps = wg ? steps1 : steps0;
       for (int i = 0; i < mysteps; ++i) {
-        const int tile = w.two ? i : 2 * i + wg, j = w.j0 + tile;
+        const int tile = w.two ? i : 2 * i + ((wg ^ t0) & 1), j = w.j0 + tile;
         const bool tree = j < w.s.tt;
-        const int first = tree ? (w.s.tt - 1 - j) * kTile : (j - w.s.tt) * kTile;
-        const int valid = min(kTile, (tree ? min(w.s.n, SV_MAX_NODES) : w.s.len) - first);
-        uint32_t see[4] = {0, 0, 0, 0};
-        if (tree) {  // ancestors that lie in this tile
-          while (up >= first) {
-            const int e = up - first;
-            if (e < kTile) {
+        const int first = (tree ? w.s.tt - 1 - j : j - w.s.tt) * kTile;
+        const int valid = (tree ? min(w.s.n, SV_MAX_NODES) : w.s.len) - first;
+        const bool special = tree || valid < kTile;
+        uint32_t see[4];
+        if (special) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if ((e >> 5) == q) see[q] |= 1u << (e & 31);
-            }
-            const int p = __ldg(parents + up);
-            if (p < -1 || p >= up) {
-              bad = true;
-              up = -1;
-            } else {
-              up = p;
-            }
+          for (int q = 0; q < 4; ++q) {
+            const int m = valid - 32 * q;
+            see[q] = tree || m <= 0 ? 0u : (m >= 32 ? 0xFFFFFFFFu : (1u << m) - 1u);
           }
-        }
-        // rows of the value tile that hold no key of this tile weigh nothing, but a weight of
-        // zero does not silence what they may hold: they are cleared, and so are infinities and
-        // NaN in the nodes' own values (added back at the end to the rows that see them)
-        if ((tree || valid < kTile) && (!w.two || wg == 0)) {
-          const int vpos = t0 + 2 * tile + 1, st = vpos % S::kStages;
-          if (alive) alive = __all_sync(0xffffffffu, wait(sh, &sh.full[st], (vpos / S::kStages) & 1));
-          if (alive) {
-            char* vt = ring + st * S::kTileBytes;
-            if (r >= valid) {
-              for (int hf = 0; hf < S::kHalves; ++hf)
-                for (int c = 0; c < 8; ++c)
-                  *reinterpret_cast<uint4*>(vt + hf * (kTile * 128) + r * 128 + ((c ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-            } else if (tree) {
-              for (int hf = 0; hf < S::kHalves; ++hf)
-                for (int c = 0; c < 8; ++c) {
-                  uint32_t* at = reinterpret_cast<uint32_t*>(vt + hf * (kTile * 128) + r * 128 + ((c ^ (r & 7)) << 4));
-                  const uint4 x = *reinterpret_cast<uint4*>(at);
-                  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+          if (tree) {  // ancestors that lie in this tile
+            while (up >= first) {
+              const int e = up - first;
+              if (e < kTile) {
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const bool lo = not_finite<kBf16>(xs[e]), hi = not_finite<kBf16>(xs[e] >> 16);
-                    if (lo || hi) {
-                      at[e] = xs[e] & (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
-                      sh.badv = 1;
-                    }
-                  }
-                }
+                for (int q = 0; q < 4; ++q)
+                  if ((e >> 5) == q) see[q] |= 1u << (e & 31);
+              }
+              const int p = __ldg(parents + up);
+              if (p < -1 || p >= up) {
+                bad = true;
+                up = -1;
+              } else {
+                up = p;
+              }
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
         }
         if (alive) alive = __all_sync(0xffffffffu, wait(sh, &sh.sfull[wg], steps_done & 1));
         ++steps_done;
         if (alive && busy) {
           tc_fence_after();
-          if (tree) {
-            weigh(std::integral_constant<int, 2>(), i == 0, mine, valid, see);
-          } else if (valid < kTile) {
-            weigh(std::integral_constant<int, 1>(), i == 0, mine, valid, nullptr);
+          if (special) {
+            weigh(std::true_type(), i == 0, mine, see);
           } else {
-            weigh(std::integral_constant<int, 0>(), i == 0, mine, valid, nullptr);
+            weigh(std::false_type(), i == 0, mine, see);
           }
           tc_fence_before();
+        }
+        if (special) {
+          // Rows of the value tile that hold no key of this tile weigh nothing, but a weight of
+          // zero does not silence what they may hold: they are cleared, and so are infinities
+          // and NaN in the nodes' own values (added back at the end to the rows that see them).
+          // With two query tiles both groups do it, to the same effect.  (Only now: S of this tile
+          // says that the value stage's last lap is over.)
+          const int st = S::stage(t0 + tile) + 1;
+          if (alive) alive = __all_sync(0xffffffffu, wait(sh, &sh.full[st], S::parity(t0 + tile)));
+          if (alive) {
+            char* vt = ring + st * S::kTileBytes + r * 128;
+#pragma unroll 1
+            for (int c = 0; c < 8 * S::kHalves; ++c) {
+              uint4* vec = reinterpret_cast<uint4*>(vt + (c >> 3) * (kTile * 128) + (((c ^ r) & 7) << 4));
+              if (r >= valid) {
+                *vec = make_uint4(0, 0, 0, 0);
+              } else if (tree) {
+                uint4 y = *vec;
+                uint32_t ys[4] = {y.x, y.y, y.z, y.w};
+                bool hit = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const bool lo = not_finite<kBf16>(ys[e]), hi = not_finite<kBf16>(ys[e] >> 16);
+                  hit |= lo || hi;
+                  ys[e] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
+                }
+                if (hit) {
+                  *vec = make_uint4(ys[0], ys[1], ys[2], ys[3]);
+                  sh.badv[buf] = 1;
+                }
+              }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
         }
         mbar_arrive(&sh.pready[wg]);
       }
       // ---- the part's result
       if (alive && mysteps > 0) alive = __all_sync(0xffffffffu, wait(sh, &sh.pvdone[wg], (steps_done - 1) & 1));
       if (bad || !alive) sum = NAN;
-      sh.xch[wg][r] = make_float2(shift, sum);
+      // (A group writes here again behind second products that wait for all warps to have left
+      // its last part with steps; badv of two parts ahead was last read two barriers ago.)
+      if (mysteps > 0) sh.xch[wg][r] = make_float2(shift, sum);
+      if (tid == 0) sh.badv[(buf + 2) & 3] = 0;
       tc_fence_before();
       soft_sync();
       tc_fence_after();
+      const bool extra = sh.badv[buf] != 0;
       const bool join = !w.two;  // both groups hold parts of the same rows
       float f0 = 1.0f, f1 = 0.0f;
       if (join) {
-        const float2 a = sh.xch[0][r], b = sh.xch[1][r];
+        const float2 a = steps0 > 0 ? sh.xch[0][r] : make_float2(-INFINITY, 0.0f);
+        const float2 b = steps1 > 0 ? sh.xch[1][r] : make_float2(-INFINITY, 0.0f);
         const float now = fmaxf(a.x, b.x);
         f0 = a.x == -INFINITY ? 0.0f : ex2_approx(a.x - now);
         f1 = b.x == -INFINITY ? 0.0f : ex2_approx(b.x - now);
         shift = now;
-        sum = f0 * a.y + (T > 1 ? f1 * b.y : 0.0f);
+        sum = f0 * a.y + f1 * b.y;
+        if (bad) sum = NAN;
       }
+      if (*const_cast<volatile int*>(&sh.badpage[dseg & 7])) sum = NAN;
       const bool whole = w.j0 == 0 && w.j1 == w.s.J;
-      const bool extra = sh.badv != 0;
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       const int slot = cta * 2 + (dseg == 0 ? 0 : 1);
       const int row = w.s.lo + node;
@@ -671,20 +673,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         for (int c = cbeg; c < cend; c += 32) {
           float o[32];
           if (alive) {
-            tmem_ld32(o_at + (join ? 0 : wg * kTile) + c, o);
+            // with one step in all, the one group's accumulator is the result
+            tmem_ld32(o_at + (join ? steps0 == 0 : wg) * kTile + c, o);
             tc_wait_ld();
-            if (join) {
-              if (T > 1) {
-                float o1[32];
-                tmem_ld32(o_at + kTile + c, o1);
-                tc_wait_ld();
+            if (join && T > 1) {
+              float o1[32];
+              tmem_ld32(o_at + kTile + c, o1);
+              tc_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = f0 * o[e] + f1 * o1[e];
-              }
+              for (int e = 0; e < 32; ++e) o[e] = f0 * o[e] + f1 * o1[e];
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = NAN;
           }
           if (extra && mine) {  // infinities and NaN among the values this row sees
             for (int a = node; a >= 0;) {
@@ -717,6 +715,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           }
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (steps0 > 0) mbar_arrive(&sh.oempty[0]);
+        if (steps1 > 0) mbar_arrive(&sh.oempty[1]);
+      }
       if (mine && (!join || wg == 0)) {
         if (whole) {
           if (P.lse) P.lse[static_cast<int64_t>(row) * P.Hq + head] = (shift + log2f(sum)) * kLn2;
@@ -724,22 +728,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           P.part_s[static_cast<int64_t>(slot * 2 + (join ? 0 : wg)) * kTile + r] = make_float2(shift, sum);
         }
       }
-      // the unit starts here and goes on behind this CTA: describe it for the join
-      if (tid == 0 && w.j0 == 0 && w.j1 < w.s.J) {
-        P.desc[cta * 2] = make_int4(w.s.lo + w.u * 2 * P.npt, min(w.s.n - w.u * 2 * P.npt, 2 * P.npt), w.h, slot);
-        P.desc[cta * 2 + 1] = make_int4(cdiv(w.s.J - w.j1, static_cast<int>(min(chunk, static_cast<int64_t>(INT_MAX)))), 0, 0, 0);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.oempty);
-      soft_sync();  // xch and badv are free again
-      t0 += 2 * T;
+      t0 += T;
       ++dseg;
     }
     if (tid == 0) {
-      // no unit is cut behind this CTA
-      const bool cut = dseg > 0 && w.j0 == 0 && w.j1 < w.s.J;
-      if (!cut) P.desc[cta * 2] = make_int4(0, 0, 0, 0);
+      // the unit that starts here and goes on behind this CTA, for the join: first node, nodes,
+      // key head, slot; parts behind this one
+      int4 d = make_int4(0, 0, 0, 0);
+      int more = 0;
+      if (dseg > 0 && w.j0 == 0 && w.j1 < w.s.J) {
+        d = make_int4(w.s.lo + w.u * 2 * P.npt, min(w.s.n - w.u * 2 * P.npt, 2 * P.npt), w.h, cta * 2 + (dseg == 1 ? 0 : 1));
+        more = static_cast<int>((w.s.J - w.j1 + chunk - 1) / chunk);
+      }
+      P.desc[cta * 2] = d;
+      P.desc[cta * 2 + 1] = make_int4(more, 0, 0, 0);
     }
   }
   tc_fence_before();
@@ -749,43 +751,108 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Join of the units that CTA borders cut: block (x, y) takes 2^10 four-column
-// groups of the unit that starts in CTA x and ends behind it.
+// Join of the units that CTA borders cut.  Every block lists the cut units
+// (one for each CTA at most) and takes its share of their items: 32 rows by
+// one group of four columns, the parts dealt to the block's eight warps, when
+// the unit has eight parts or more, else 32 rows by eight column groups, one
+// a warp.  Parts are added in a fixed order.
+constexpr int kJoinThreads = 256;
 template <int DP, bool kBf16>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ AttnParams P) {
+  __shared__ int first[kJoinThreads];   // first item behind each unit
+  __shared__ int wsum[8];
+  __shared__ float4 acc_s[8][32];
+  __shared__ float2 st_s[8][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int last_row = P.npt * P.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int cta = blockIdx.x;
-  const int4 d = P.desc[cta * 2];
-  const int nodes = d.y;
-  if (nodes == 0) return;
-  const int more = P.desc[cta * 2 + 1].x;  // parts behind the first
-  const int idx = blockIdx.y * 256 + threadIdx.x;
-  const int r2 = idx % (2 * kTile), cg = idx / (2 * kTile);  // row of the two tiles, column group
-  const int tile = r2 / kTile, r = r2 - tile * kTile;
-  const int rnode = r / P.G, rg = r - rnode * P.G;
-  if (rnode >= P.npt || tile * P.npt + rnode >= nodes || cg >= DP / 4) return;
-  auto at = [&](int p) { return (p == 0 ? d.w : (cta + p) * 2) * 2 + tile; };
-  float top = -INFINITY;
-  for (int p = 0; p <= more; ++p) top = fmaxf(top, P.part_s[static_cast<int64_t>(at(p)) * kTile + r].x);
-  float sum = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int p = 0; p <= more; ++p) {
-    const float2 s = P.part_s[static_cast<int64_t>(at(p)) * kTile + r];
-    const float4 x = reinterpret_cast<const float4*>(P.part_o)[(static_cast<int64_t>(at(p)) * (DP / 4) + cg) * kTile + r];
-    const float f = s.x == -INFINITY ? 0.0f : ex2_approx(s.x - top);
-    sum += f * s.y;
-    o.x += f * x.x;
-    o.y += f * x.y;
-    o.z += f * x.z;
-    o.w += f * x.w;
+  int items = 0;
+  if (tid < P.ctas) {
+    const int nodes = P.desc[tid * 2].y, more = P.desc[tid * 2 + 1].x;
+    const int blocks = nodes == 0 ? 0 : nodes > P.npt ? 4 + cdiv((nodes - P.npt) * P.G, 32) : cdiv(nodes * P.G, 32);
+    items = blocks * (more + 1 >= 8 ? DP / 4 : DP / 32);
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int64_t row = static_cast<int64_t>(d.x + tile * P.npt + rnode) * P.Hq + d.z * P.G + rg;
-  if (cg * 4 < P.D)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + row * P.D + cg * 4) =
-        make_uint2(pack2<kBf16>(o.x * inv, o.y * inv), pack2<kBf16>(o.z * inv, o.w * inv));
-  if (P.lse && cg == 0) P.lse[row] = (top + log2f(sum)) * kLn2;
+  int incl = items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) incl += wsum[i];
+  first[tid] = incl;
+  __syncthreads();
+  const int total = first[kJoinThreads - 1];
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    int lo = 0, hi = kJoinThreads - 1;  // the unit
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] > item) {
+        hi = mid;
+      } else {
+        lo = mid + 1;
+      }
+    }
+    const int cta = lo;
+    const int4 d = P.desc[cta * 2];
+    const int parts = P.desc[cta * 2 + 1].x + 1;
+    const int k = item - (cta > 0 ? first[cta - 1] : 0);
+    const bool split = parts >= 8;
+    const int cgs = split ? DP / 4 : DP / 32;
+    const int rb = k / cgs, cg = split ? k - rb * cgs : (k - rb * cgs) * 8 + warp;
+    const int tile = rb >> 2, r = (rb & 3) * 32 + lane;
+    const int rnode = r / P.G, rg = r - rnode * P.G;
+    const bool mine = r < last_row && tile * P.npt + rnode < d.y;
+    auto at = [&](int p) { return static_cast<int64_t>((p == 0 ? d.w : (cta + p) * 2) * 2 + tile); };
+    float top = -INFINITY, sum = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (mine) {
+      const int p0 = split ? warp : 0, step = split ? 8 : 1;
+#pragma unroll 4
+      for (int p = p0; p < parts; p += step) top = fmaxf(top, P.part_s[at(p) * kTile + r].x);
+#pragma unroll 4
+      for (int p = p0; p < parts; p += step) {
+        const float2 s = P.part_s[at(p) * kTile + r];
+        const float4 x = reinterpret_cast<const float4*>(P.part_o)[(at(p) * (DP / 4) + cg) * kTile + r];
+        const float f = s.x == -INFINITY ? 0.0f : ex2_approx(s.x - top);
+        sum += f * s.y;
+        o.x += f * x.x;
+        o.y += f * x.y;
+        o.z += f * x.z;
+        o.w += f * x.w;
+      }
+    }
+    if (split) {
+      acc_s[warp][lane] = o;
+      st_s[warp][lane] = make_float2(top, sum);
+      __syncthreads();
+      if (warp == 0) {
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, st_s[i][lane].x);
+        sum = 0.0f;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i = 0; i < 8; ++i) {
+          const float2 s = st_s[i][lane];
+          const float4 x = acc_s[i][lane];
+          const float f = s.x == -INFINITY ? 0.0f : ex2_approx(s.x - top);
+          sum += f * s.y;
+          o.x += f * x.x;
+          o.y += f * x.y;
+          o.z += f * x.z;
+          o.w += f * x.w;
+        }
+      }
+    }
+    if (mine && (!split || warp == 0)) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const int64_t row = static_cast<int64_t>(d.x + tile * P.npt + rnode) * P.Hq + d.z * P.G + rg;
+      if (cg * 4 < P.D)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + row * P.D + cg * 4) =
+            make_uint2(pack2<kBf16>(o.x * inv, o.y * inv), pack2<kBf16>(o.z * inv, o.w * inv));
+      if (P.lse && cg == 0) P.lse[row] = (top + log2f(sum)) * kLn2;
+    }
+    if (split) __syncthreads();
+  }
 }
 
 // ---------------------------------------------------------------------- host
@@ -876,8 +943,8 @@ int launch_attn(const AttnParams& p, int ctas, cudaStream_t stream) {
   int rc = check_launch("tree attention");
   if (rc != SV_OK) return rc;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, DP / 4 * 2 * kTile / 256);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(ctas * 4);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -994,6 +1061,7 @@ int spec_tree_attention(const sv_tree_attention_args* a, void* workspace, size_t
   p.width = a->table_width;
   p.box = box;
   p.npt = npt;
+  p.ctas = ctas;
   p.sl = a->scale * kLog2e;
   char* ws = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws + lay.o);
