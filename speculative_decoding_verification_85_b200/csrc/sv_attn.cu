@@ -137,16 +137,27 @@ struct Walk {
   }
 };
 
+// One part as the other warps read it: the key warp walks the line and leaves
+// every part's description in a ring of kParts.
+struct alignas(16) Part {
+  int lo, n, len, tt;     // first packed row, nodes, cached tokens, tree tiles
+  int h, u, j0, j1;       // key head, unit within the head, tiles of the unit
+  int J, b, two, mark;    // tiles of the whole unit, sequence; two query tiles; marked; b < 0: the end
+};
+constexpr int kParts = 8;
+
 struct Shared {
   uint64_t full[8], empty[8];
-  uint64_t qfull[2], sfull[2], pready[2], pvdone[2], oempty[2], drain[2], meet;
+  uint64_t qfull[2], sfull[2], pready[2], pvdone[2], oempty[2], turn[2], drain[2], meet, met;
   float2 xch[2][kTile];       // [group][row]: shift, sum
   int64_t scan[16];
   Walk start;
   uint32_t tmem;
   int dead;
   int badv[4];                // [part & 3]: a tree tile holds infinities or NaN among its values
-  int badpage[8];             // [part & 7]: a page outside the cache
+  int badpage[kParts];        // a page outside the cache
+  uint64_t parted[kParts], freed[kParts];  // the part is described; all readers are done with it
+  Part parts[kParts];
 };
 
 // Wait for a phase; false once any wait of the CTA has run out of time.
@@ -168,8 +179,6 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity)
     if (mbar_try_wait(bar, parity)) return true;
   return wait_long(sh, bar, parity);
 }
-
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -207,6 +216,11 @@ __device__ __forceinline__ bool not_finite(uint32_t half) {
   return (half & kExpMask<kBf16>) == kExpMask<kBf16>;
 }
 template <bool kBf16>
+__device__ __forceinline__ bool any_not_finite(const uint4& y) {
+  constexpr uint32_t m = kExpMask<kBf16> * 0x10001u;
+  return (__vcmpeq2(y.x & m, m) | __vcmpeq2(y.y & m, m) | __vcmpeq2(y.z & m, m) | __vcmpeq2(y.w & m, m)) != 0;
+}
+template <bool kBf16>
 __device__ __forceinline__ float widen(uint32_t half) {
   if constexpr (kBf16) return __uint_as_float(half << 16);
   float f;
@@ -235,9 +249,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       mbar_init(&sh.pready[i], kTile);
       mbar_init(&sh.pvdone[i], 1);
       mbar_init(&sh.oempty[i], kWarpsSoft);
+      mbar_init(&sh.turn[i], kWarpsSoft / 2);
       mbar_init(&sh.drain[i], 1);
     }
     mbar_init(&sh.meet, 2);
+    mbar_init(&sh.met, kWarpsSoft);
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(&sh.parted[i], 1);
+      mbar_init(&sh.freed[i], kWarpsSoft + 3);  // softmax, values and products
+    }
     for (int i = 0; i < 4; ++i) sh.badv[i] = 0;
     mbar_init_fence();
     sh.dead = 0;
@@ -304,9 +324,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   __syncthreads();
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;");
-  Walk w{};
-  if (begin < total) w = sh.start;  // else nothing is left for this CTA
   const uint32_t tmem = sh.tmem;
+  // Part `seg`; every reader takes them all, in order, and gives each back (freed).
+  auto part_of = [&](int seg, Part& w) {
+    const bool ok = wait(sh, &sh.parted[seg % kParts], (seg / kParts) & 1);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    const int4* d = reinterpret_cast<const int4*>(&sh.parts[seg % kParts]);
+    int4* o = reinterpret_cast<int4*>(&w);
+    o[0] = d[0];
+    o[1] = d[1];
+    o[2] = d[2];
+    return w.b >= 0;
+  };
 
   if (warp >= kWarpsSoft) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
@@ -318,28 +347,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const CUtensorMap* cached = kv ? &P.vcmap : &P.kcmap;
       int t = 0, seg = 0;
       bool ok = true;
-      while (ok && w.next(P)) {
+      Walk walk{};
+      if (begin < total) walk = sh.start;  // else nothing is left for this CTA
+      for (;; ++seg) {
+        Part w;
+        if (kv) {
+          if (!part_of(seg, w)) break;
+          if (lane == 0) mbar_arrive(&sh.freed[seg % kParts]);
+        } else {
+          w.b = -1;
+          ok = ok && __all_sync(0xffffffffu, wait(sh, &sh.freed[seg % kParts], ((seg / kParts) & 1) ^ 1));
+          if (!ok) break;
+          if (walk.next(P))
+            w = {walk.s.lo, walk.s.n, walk.s.len, walk.s.tt, walk.h, walk.u, walk.j0, walk.j1, walk.s.J, walk.b, walk.two, walk.s.mark};
+          if (lane == 0) {
+            sh.badpage[seg % kParts] = 0;
+            sh.parts[seg % kParts] = w;
+            mbar_arrive(&sh.parted[seg % kParts]);
+          }
+          __syncwarp();
+          if (w.b < 0) break;
+          // the parents' lines, which the softmax warps will walk
+          if (w.j0 < w.tt && lane * 32 < w.n)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(P.parents + w.lo + lane * 32));
+        }
         const int32_t* row = P.table + w.b * P.table_row;
         // this lane's page of a context tile (read a tile ahead): its load's page where pages
         // are smaller than a tile, else the tile's
         const int per = kTile / P.box, span = P.page / P.box;
         auto page_at = [&](int j) {
-          const int c = j - w.s.tt;
-          if (c < 0 || j >= w.j1 || lane >= per || c * kTile + lane * P.box >= w.s.len) return 0;
+          const int c = j - w.tt;
+          if (c < 0 || j >= w.j1 || lane >= per || c * kTile + lane * P.box >= w.len) return 0;
           return row[span == 1 ? c * per + lane : c / span];
         };
         int page = page_at(w.j0);
-        if (!kv && lane == 0) sh.badpage[seg & 7] = 0;
-        __syncwarp();
         for (int j = w.j0; j < w.j1; ++j) {
           const int ahead = page_at(j + 1);
-          const bool tree = j < w.s.tt;
-          const int c = tree ? w.s.tt - 1 - j : j - w.s.tt;  // tile of the tree, of the context
-          const int valid = min(kTile, (tree ? min(w.s.n, SV_MAX_NODES) : w.s.len) - c * kTile);
+          const bool tree = j < w.tt;
+          const int c = tree ? w.tt - 1 - j : j - w.tt;  // tile of the tree, of the context
+          const int valid = min(kTile, (tree ? min(w.n, SV_MAX_NODES) : w.len) - c * kTile);
           const int rows = tree ? kTreeBox : P.box;
           const int boxes = (valid + rows - 1) / rows;
           if (page < 0 || page >= P.num_pages) {
-            if (!kv) sh.badpage[seg & 7] = 1;  // the rows will be marked
+            if (!kv) sh.badpage[seg % kParts] = 1;  // the rows will be marked
             page = 0;
           }
           const int st = S::stage(t) + (kv ? 1 : 0);
@@ -352,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             if (tree) {
 #pragma unroll
               for (int hf = 0; hf < S::kHalves; ++hf)
-                tma_3d(dst + hf * (kTile * 128), own, hf * 64, w.h, w.s.lo + c * kTile + lane * kTreeBox, &sh.full[st]);
+                tma_3d(dst + hf * (kTile * 128), own, hf * 64, w.h, w.lo + c * kTile + lane * kTreeBox, &sh.full[st]);
             } else {
               const int tok = span == 1 ? 0 : (c % span) * kTile;
 #pragma unroll
@@ -364,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           page = ahead;
           ++t;
         }
-        ++seg;
+        if (!ok) break;
       }
       if (!ok) {  // leave no copy in flight behind
         for (int i = max(0, t - S::kPairs); i < t; ++i) {
@@ -392,30 +442,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       // second products, query tiles loaded, parts with steps, parts with two query tiles so far
       uint32_t npv = 0, nq = 0, nown = 0, ntwo = 0;
       // steps of this group in the part that begins at tile t
-      auto steps_of = [&](const Walk& x, int t) {
+      auto steps_of = [&](const Part& x, int t) {
         const int T = x.j1 - x.j0;
         return x.two ? T : (T + 1 - ((s ^ t) & 1)) / 2;
       };
-      auto load_q = [&](const Walk& x) {
+      auto load_q = [&](const Part& x) {
         if (issuer) {
           mbar_arrive_expect_tx(&sh.qfull[s], P.npt * P.G * 128 * S::kHalves);
 #pragma unroll
           for (int hf = 0; hf < S::kHalves; ++hf)
             tma_3d(qtile + s * S::kTileBytes + hf * (kTile * 128), &P.qmap, hf * 64, x.h * P.G,
-                   x.s.lo + (x.u * 2 + (x.two ? s : 0)) * P.npt, &sh.qfull[s]);
+                   x.lo + (x.u * 2 + (x.two ? s : 0)) * P.npt, &sh.qfull[s]);
         }
         __syncwarp();
         ++nq;
       };
       bool ok = true;
-      bool more = w.next(P);
+      int seg = 0;
+      Part w;
+      auto next_part = [&]() {
+        const bool got = part_of(seg, w);
+        if (issuer && got) mbar_arrive(&sh.freed[seg % kParts]);
+        ++seg;
+        return got;
+      };
+      bool more = next_part();
       if (more && steps_of(w, 0)) load_q(w);
       while (ok && more) {
         const bool two = w.two;
         const int steps = steps_of(w, t0), stride = two ? 1 : 2;
         int t = two ? t0 : t0 + ((s ^ t0) & 1);  // own tile
         t0 += w.j1 - w.j0;
-        more = w.next(P);
         auto scores = [&]() {  // S of tile t
           const int st = S::stage(t);
           if (!__all_sync(0xffffffffu, wait(sh, &sh.full[st], S::parity(t)))) return false;
@@ -467,7 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           if (i + 1 < steps) ok = __all_sync(0xffffffffu, wait(sh, &sh.pvdone[s], (npv - 1) & 1)) && scores();
         }
         // the part's last S is done: its query tile can go
-        if (ok && more && steps_of(w, t0)) load_q(w);
+        more = ok && next_part();
+        if (more && steps_of(w, t0)) load_q(w);
       }
       if (!ok) {  // let the products and the copy in flight end
         if (issuer) mma_commit(&sh.drain[s]);
@@ -489,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const float sl = P.sl;
     int t0 = 0, dseg = 0;       // tiles and parts so far
     uint32_t steps_done = 0;    // steps of this group so far
+    uint32_t turns = 0;         // turns of this group so far
     bool alive = true;
     float shift = 0.0f, sum = 0.0f;  // this row's exponent shift (base 2) and sum of weights
 
@@ -547,13 +606,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       tc_wait_st();
     };
 
-    while (w.next(P)) {
+    Part w;
+    bool cut = false;  // the last part's unit starts here and goes on behind this CTA
+    int4 cut_at = make_int4(0, 0, 0, 0);
+    int cut_left = 0;
+    while (alive && part_of(dseg, w)) {
       const int T = w.j1 - w.j0, buf = dseg & 3;
       const int node = w.u * 2 * P.npt + (w.two ? wg * P.npt : 0) + rnode;  // within the sequence
-      const bool mine = rnode < P.npt && node < w.s.n;
+      const bool mine = rnode < P.npt && node < w.n;
       const bool busy = __any_sync(0xffffffffu, mine);  // does this warp hold a row at all
-      const int32_t* parents = P.parents + w.s.lo;
-      bool bad = w.s.mark;
+      const int32_t* parents = P.parents + w.lo;
+      bool bad = w.mark;
       shift = -INFINITY;
       sum = 0.0f;
       int up = mine ? node : -1;  // next ancestor to pass
@@ -562,9 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const int mysteps = wg ? steps1 : steps0;
       for (int i = 0; i < mysteps; ++i) {
         const int tile = w.two ? i : 2 * i + ((wg ^ t0) & 1), j = w.j0 + tile;
-        const bool tree = j < w.s.tt;
-        const int first = (tree ? w.s.tt - 1 - j : j - w.s.tt) * kTile;
-        const int valid = (tree ? min(w.s.n, SV_MAX_NODES) : w.s.len) - first;
+        const bool tree = j < w.tt;
+        const int first = (tree ? w.tt - 1 - j : j - w.tt) * kTile;
+        const int valid = (tree ? min(w.n, SV_MAX_NODES) : w.len) - first;
         const bool special = tree || valid < kTile;
         uint32_t see[4];
         if (special) {
@@ -591,9 +654,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
           }
         }
-        if (alive) alive = __all_sync(0xffffffffu, wait(sh, &sh.sfull[wg], steps_done & 1));
+        alive = wait(sh, &sh.sfull[wg], steps_done & 1);
+        // with two query tiles the groups take turns, so that one's exponentials run beside the
+        // other's products: group 0's turn k + 1 follows group 1's turn k
+        if (w.two && (wg || turns > 0)) alive = alive && wait(sh, &sh.turn[wg], (turns - (wg ? 0 : 1)) & 1);
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) break;
         ++steps_done;
-        if (alive && busy) {
+        if (busy) {
           tc_fence_after();
           if (special) {
             weigh(std::true_type(), i == 0, mine, see);
@@ -602,6 +670,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           }
           tc_fence_before();
         }
+        if (w.two) {
+          ++turns;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.turn[wg ^ 1]);
+        }
         if (special) {
           // Rows of the value tile that hold no key of this tile weigh nothing, but a weight of
           // zero does not silence what they may hold: they are cleared, and so are infinities
@@ -609,27 +682,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           // With two query tiles both groups do it, to the same effect.  (Only now: S of this tile
           // says that the value stage's last lap is over.)
           const int st = S::stage(t0 + tile) + 1;
-          if (alive) alive = __all_sync(0xffffffffu, wait(sh, &sh.full[st], S::parity(t0 + tile)));
-          if (alive) {
+          alive = __all_sync(0xffffffffu, wait(sh, &sh.full[st], S::parity(t0 + tile)));
+          if (!alive) break;
+          {
             char* vt = ring + st * S::kTileBytes + r * 128;
-#pragma unroll 1
-            for (int c = 0; c < 8 * S::kHalves; ++c) {
-              uint4* vec = reinterpret_cast<uint4*>(vt + (c >> 3) * (kTile * 128) + (((c ^ r) & 7) << 4));
-              if (r >= valid) {
-                *vec = make_uint4(0, 0, 0, 0);
-              } else if (tree) {
-                uint4 y = *vec;
-                uint32_t ys[4] = {y.x, y.y, y.z, y.w};
-                bool hit = false;
+            if (r >= valid) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const bool lo = not_finite<kBf16>(ys[e]), hi = not_finite<kBf16>(ys[e] >> 16);
-                  hit |= lo || hi;
-                  ys[e] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
-                }
-                if (hit) {
-                  *vec = make_uint4(ys[0], ys[1], ys[2], ys[3]);
-                  sh.badv[buf] = 1;
+              for (int c = 0; c < 8 * S::kHalves; ++c)
+                *reinterpret_cast<uint4*>(vt + (c >> 3) * (kTile * 128) + (((c ^ r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            } else if (tree) {
+              bool hit = false;
+#pragma unroll
+              for (int c = 0; c < 8 * S::kHalves; ++c) {
+                const uint4 y = *reinterpret_cast<const uint4*>(vt + (c >> 3) * (kTile * 128) + (((c ^ r) & 7) << 4));
+                hit |= any_not_finite<kBf16>(y);
+              }
+              if (hit) {
+                sh.badv[buf] = 1;
+                for (int c = 0; c < 64 * S::kHalves; ++c) {
+                  uint16_t* v = reinterpret_cast<uint16_t*>(vt + (c >> 6) * (kTile * 128)) + (c & 63);
+                  if (not_finite<kBf16>(*v)) *v = 0;
                 }
               }
             }
@@ -640,13 +712,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       }
       // ---- the part's result
       if (alive && mysteps > 0) alive = __all_sync(0xffffffffu, wait(sh, &sh.pvdone[wg], (steps_done - 1) & 1));
-      if (bad || !alive) sum = NAN;
+      if (!alive) break;
+      if (bad) sum = NAN;
       // (A group writes here again behind second products that wait for all warps to have left
-      // its last part with steps; badv of two parts ahead was last read two barriers ago.)
+      // its last part with steps; badv of two parts ahead was last read two meetings ago.)
       if (mysteps > 0) sh.xch[wg][r] = make_float2(shift, sum);
       if (tid == 0) sh.badv[(buf + 2) & 3] = 0;
       tc_fence_before();
-      soft_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.met);
+      alive = __all_sync(0xffffffffu, wait(sh, &sh.met, dseg & 1));
+      if (!alive) break;
       tc_fence_after();
       const bool extra = sh.badv[buf] != 0;
       const bool join = !w.two;  // both groups hold parts of the same rows
@@ -661,18 +737,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         sum = f0 * a.y + f1 * b.y;
         if (bad) sum = NAN;
       }
-      if (*const_cast<volatile int*>(&sh.badpage[dseg & 7])) sum = NAN;
-      const bool whole = w.j0 == 0 && w.j1 == w.s.J;
+      if (*const_cast<volatile int*>(&sh.badpage[dseg % kParts])) sum = NAN;
+      const bool whole = w.j0 == 0 && w.j1 == w.J;
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       const int slot = cta * 2 + (dseg == 0 ? 0 : 1);
-      const int row = w.s.lo + node;
+      const int row = w.lo + node;
       const int head = w.h * P.G + rg;
       const int cbeg = join ? wg * (DP / 2) : 0, cend = join ? cbeg + DP / 2 : DP;
       if (busy) {
 #pragma unroll 1
         for (int c = cbeg; c < cend; c += 32) {
           float o[32];
-          if (alive) {
+          {
             // with one step in all, the one group's accumulator is the result
             tmem_ld32(o_at + (join ? steps0 == 0 : wg) * kTile + c, o);
             tc_wait_ld();
@@ -686,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           }
           if (extra && mine) {  // infinities and NaN among the values this row sees
             for (int a = node; a >= 0;) {
-              const uint16_t* vr = P.v + (w.s.lo + a) * P.v_node + w.h * P.v_head;
+              const uint16_t* vr = P.v + (w.lo + a) * P.v_node + w.h * P.v_head;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (c + e < P.D) {
@@ -728,25 +804,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           P.part_s[static_cast<int64_t>(slot * 2 + (join ? 0 : wg)) * kTile + r] = make_float2(shift, sum);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.freed[dseg % kParts]);
       t0 += T;
       ++dseg;
+      cut = w.j0 == 0 && w.j1 < w.J;
+      cut_at = make_int4(w.lo + w.u * 2 * P.npt, min(w.n - w.u * 2 * P.npt, 2 * P.npt), w.h, slot);
+      cut_left = w.J - w.j1;
     }
     if (tid == 0) {
-      // the unit that starts here and goes on behind this CTA, for the join: first node, nodes,
-      // key head, slot; parts behind this one
-      int4 d = make_int4(0, 0, 0, 0);
-      int more = 0;
-      if (dseg > 0 && w.j0 == 0 && w.j1 < w.s.J) {
-        d = make_int4(w.s.lo + w.u * 2 * P.npt, min(w.s.n - w.u * 2 * P.npt, 2 * P.npt), w.h, cta * 2 + (dseg == 1 ? 0 : 1));
-        more = static_cast<int>((w.s.J - w.j1 + chunk - 1) / chunk);
-      }
-      P.desc[cta * 2] = d;
+      // for the join: the cut unit's first node, nodes, key head, slot; parts behind this one
+      const int more = cut ? static_cast<int>((cut_left + chunk - 1) / chunk) : 0;
+      P.desc[cta * 2] = cut ? cut_at : make_int4(0, 0, 0, 0);
       P.desc[cta * 2 + 1] = make_int4(more, 0, 0, 0);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (sh.dead) {  // a wait ran out: NaN for every row of this CTA's parts
+    Walk k{};
+    if (begin < total) k = sh.start;
+    for (int seg = 0; k.next(P); ++seg) {
+      const bool whole = k.j0 == 0 && k.j1 == k.s.J;
+      const int slot = cta * 2 + (seg == 0 ? 0 : 1), from = k.u * 2 * P.npt;
+      const int rows = min(k.s.n - from, 2 * P.npt) * P.G;
+      for (int i = tid; i < rows; i += kThreads) {
+        const int64_t row = static_cast<int64_t>(k.s.lo + from + i / P.G) * P.Hq + k.h * P.G + i % P.G;
+        if (whole) {
+          for (int e = 0; e < P.D; ++e) static_cast<uint16_t*>(P.out)[row * P.D + e] = 0x7FFF;
+          if (P.lse) P.lse[row] = NAN;
+        } else {
+          const int tile = i / (P.npt * P.G);
+          P.part_s[static_cast<int64_t>(slot * 2 + tile) * kTile + i - tile * P.npt * P.G] = make_float2(0.0f, NAN);
+        }
+      }
+      if (tid == 0) {
+        const bool cut = k.j0 == 0 && k.j1 < k.s.J;
+        P.desc[cta * 2] = cut ? make_int4(k.s.lo + from, min(k.s.n - from, 2 * P.npt), k.h, slot) : make_int4(0, 0, 0, 0);
+        P.desc[cta * 2 + 1] = make_int4(cut ? static_cast<int>((k.s.J - k.j1 + chunk - 1) / chunk) : 0, 0, 0, 0);
+      }
+    }
+  }
   if (warp == kWarpMma)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
