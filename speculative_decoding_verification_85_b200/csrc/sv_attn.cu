@@ -48,6 +48,7 @@ constexpr int kThreads = 32 * 12;
 constexpr int kRegsSoft = 208, kRegsRest = 88;
 constexpr float kGrow = 8.0f;       // base-2 growth of a maximum that is let stand
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxCtas = 160;         // SMs of a device, with room
 constexpr int kTreeBox = 16;        // rows of one load of the nodes' own keys and values
 
 // Ring of key and value tiles.  Tile t of the CTA goes to pair t % kPairs: its
@@ -151,7 +152,8 @@ struct Shared {
   uint64_t qfull[2], sfull[2], pready[2], pvdone[2], oempty[2], turn[2], drain[2], meet, met;
   float2 xch[2][kTile];       // [group][row]: shift, sum
   int64_t scan[16];
-  Walk start;
+  Walk start;                 // the stretch (left == 0: nothing for this CTA)
+  int64_t chunk;              // tiles of a stretch
   uint32_t tmem;
   int dead;
   int badv[4];                // [part & 3]: a tree tile holds infinities or NaN among its values
@@ -272,55 +274,64 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   }
   tc_fence_before();
 
-  // ---- where this CTA's stretch begins: prefix sums of the sequences' tiles
-  int64_t total = 0, chunk = 0, begin = 0;
-  for (int pass = 0; pass < 2; ++pass) {  // the total, then the sequence that `begin` lies in
-    int64_t carry = 0;
-    for (int base = 0; base < P.B; base += kThreads) {
-      const int b = base + tid;
-      Seq s{};
-      if (b < P.B) s = seq_of(P, b);
-      const int64_t mine = static_cast<int64_t>(s.J) * s.U * P.Hkv;
-      int64_t incl = mine;
+  // ---- where this CTA's stretch begins: prefix sums of the sequences' tiles.  The key warp
+  // alone walks the line; for a few sequences it also finds the start alone, while the others
+  // set up, else the whole block does.
+  const bool few = P.B <= 128;
+  auto find_start = [&](auto wide) {
+    constexpr bool kWide = decltype(wide)::value;
+    constexpr int kLanes = kWide ? kThreads : 32;
+    const int me = kWide ? tid : lane;
+    int64_t total = 0, chunk = 0, begin = 0;
+    if (me == 0) sh.start.left = 0;
+    __syncwarp();
+    for (int pass = 0; pass < 2; ++pass) {  // the total, then the sequence that `begin` lies in
+      int64_t carry = 0;
+#pragma unroll 1
+      for (int base = 0; base < P.B; base += kLanes) {
+        const int b = base + me;
+        Seq s{};
+        if (b < P.B) s = seq_of(P, b);
+        const int64_t mine = static_cast<int64_t>(s.J) * s.U * P.Hkv;
+        int64_t incl = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      __syncthreads();
-      if (lane == 31) sh.scan[warp] = incl;
-      __syncthreads();
-      int64_t before = carry;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += sh.scan[w];
-        carry += sh.scan[w];
-      }
-      incl += before;
-      if (P.B <= kThreads || pass == 1) {
-        if (pass == 0) {
-          total = carry;
-          chunk = (total + gridDim.x - 1) / gridDim.x;
-          begin = cta * chunk;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
         }
-        if (mine > 0 && incl - mine <= begin && begin < incl) {
-          Walk w{};
-          int64_t at = begin - (incl - mine);
-          w.b = b;
-          w.s = s;
-          w.hu = static_cast<int>(at / s.J);
-          w.j = static_cast<int>(at - static_cast<int64_t>(w.hu) * s.J);
-          w.left = min(chunk, total - begin);
-          sh.start = w;
+        int64_t sum = __shfl_sync(0xffffffffu, incl, 31);
+        if constexpr (kWide) {
+          __syncthreads();
+          if (lane == 31) sh.scan[warp] = incl;
+          __syncthreads();
+          sum = 0;
+          for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) incl += sh.scan[i];
+            sum += sh.scan[i];
+          }
+        }
+        incl += carry;
+        carry += sum;
+        if (pass == 1 && mine > 0 && incl - mine <= begin && begin < incl) {
+          Walk k{};
+          const int64_t at = begin - (incl - mine);
+          k.b = b;
+          k.s = s;
+          k.hu = static_cast<int>(at / s.J);
+          k.j = static_cast<int>(at - static_cast<int64_t>(k.hu) * s.J);
+          k.left = min(chunk, total - begin);
+          sh.start = k;
         }
       }
+      if (pass == 0) {
+        total = carry;
+        chunk = (total + gridDim.x - 1) / gridDim.x;
+        begin = cta * chunk;
+      }
     }
-    if (pass == 0) {
-      total = carry;
-      chunk = (total + gridDim.x - 1) / gridDim.x;
-      begin = cta * chunk;
-      if (P.B <= kThreads) break;
-    }
-  }
+    if (me == 0) sh.chunk = chunk;
+  };
+  if (!few) find_start(std::true_type());
   __syncthreads();
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;");
@@ -348,7 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       int t = 0, seg = 0;
       bool ok = true;
       Walk walk{};
-      if (begin < total) walk = sh.start;  // else nothing is left for this CTA
+      if (!kv) {
+        if (few) find_start(std::false_type());
+        __syncwarp();
+        walk = sh.start;
+      }
       for (;; ++seg) {
         Part w;
         if (kv) {
@@ -552,17 +567,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     float shift = 0.0f, sum = 0.0f;  // this row's exponent shift (base 2) and sum of weights
 
     // S of one key tile to P: shift, sum and, when a maximum has grown much, the accumulator.
-    // kMasked: only the keys in `see` count.
-    auto weigh = [&](auto masked, bool fresh, bool mine, const uint32_t* see) {
+    // With two query tiles the groups take turns at the exponentials, so that one's run beside
+    // the other's products: group 0's turn k + 1 follows group 1's turn k.  False: a wait failed.
+    auto weigh = [&](bool fresh, bool mine, bool two) {
       float x[kTile];
 #pragma unroll
       for (int c = 0; c < kTile; c += 32) tmem_ld32(s_at + c, x + c);
       tc_wait_ld();
-      if constexpr (decltype(masked)::value) {
-#pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          if (!(see[c >> 5] >> (c & 31) & 1)) x[c] = -INFINITY;
-      }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int c = 0; c < kTile; c += 2) mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], x[c]), x[c + 1]);
@@ -584,6 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           tmem_st16(o_at + wg * kTile + c, reinterpret_cast<uint32_t*>(o));
         }
       }
+      if (two && (wg || turns > 0) && !__all_sync(0xffffffffu, wait(sh, &sh.turn[wg], (turns - (wg ? 0 : 1)) & 1)))
+        return false;
       const float neg = shift == -INFINITY ? 0.0f : -shift;
       const uint64_t sl2 = pair(sl, sl), neg2 = pair(neg, neg);
       uint64_t part[2] = {0, 0};
@@ -604,6 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const uint64_t p = add2(part[0], part[1]);
       sum += pair_lo(p) + pair_hi(p);
       tc_wait_st();
+      return true;
     };
 
     Part w;
@@ -654,22 +668,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
           }
         }
-        alive = wait(sh, &sh.sfull[wg], steps_done & 1);
-        // with two query tiles the groups take turns, so that one's exponentials run beside the
-        // other's products: group 0's turn k + 1 follows group 1's turn k
-        if (w.two && (wg || turns > 0)) alive = alive && wait(sh, &sh.turn[wg], (turns - (wg ? 0 : 1)) & 1);
-        alive = __all_sync(0xffffffffu, alive);
+        alive = __all_sync(0xffffffffu, wait(sh, &sh.sfull[wg], steps_done & 1));
         if (!alive) break;
         ++steps_done;
         if (busy) {
           tc_fence_after();
-          if (special) {
-            weigh(std::true_type(), i == 0, mine, see);
-          } else {
-            weigh(std::false_type(), i == 0, mine, see);
+          if (special) {  // -inf for the keys that do not count
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t m = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
+              float x[32];
+              tmem_ld32(s_at + 32 * q, x);
+              tc_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(m >> c & 1)) x[c] = -INFINITY;
+              tmem_st32(s_at + 32 * q, reinterpret_cast<uint32_t*>(x));
+            }
+            tc_wait_st();
           }
+          alive = weigh(i == 0, mine, w.two);
           tc_fence_before();
+        } else if (w.two && (wg || turns > 0)) {
+          alive = __all_sync(0xffffffffu, wait(sh, &sh.turn[wg], (turns - (wg ? 0 : 1)) & 1));
         }
+        if (!alive) break;
         if (w.two) {
           ++turns;
           __syncwarp();
@@ -746,25 +769,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const int cbeg = join ? wg * (DP / 2) : 0, cend = join ? cbeg + DP / 2 : DP;
       if (busy) {
 #pragma unroll 1
-        for (int c = cbeg; c < cend; c += 32) {
-          float o[32];
-          {
-            // with one step in all, the one group's accumulator is the result
-            tmem_ld32(o_at + (join ? steps0 == 0 : wg) * kTile + c, o);
+        for (int c = cbeg; c < cend; c += 16) {
+          // with steps of one group alone, its accumulator is the result
+          float o[16];
+          tmem_ld16(o_at + (join ? steps0 == 0 : wg) * kTile + c, o);
+          if (join && T > 1) {
+            float o1[16];
+            tmem_ld16(o_at + kTile + c, o1);
             tc_wait_ld();
-            if (join && T > 1) {
-              float o1[32];
-              tmem_ld32(o_at + kTile + c, o1);
-              tc_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = f0 * o[e] + f1 * o1[e];
-            }
+            for (int e = 0; e < 16; ++e) o[e] = f0 * o[e] + f1 * o1[e];
+          } else {
+            tc_wait_ld();
           }
           if (extra && mine) {  // infinities and NaN among the values this row sees
             for (int a = node; a >= 0;) {
               const uint16_t* vr = P.v + (w.lo + a) * P.v_node + w.h * P.v_head;
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
+              for (int e = 0; e < 16; ++e)
                 if (c + e < P.D) {
                   const uint32_t x = __ldg(vr + c + e);
                   if (not_finite<kBf16>(x)) o[e] += widen<kBf16>(x);
@@ -773,20 +795,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
               a = p < a ? p : -1;
             }
           }
-          if (mine) {
+          if (mine && c < P.D) {
             if (whole) {
-              uint16_t* out = static_cast<uint16_t*>(P.out) + (static_cast<int64_t>(row) * P.Hq + head) * P.D + c;
+              uint32_t y[8];
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                if (c + e < P.D)
-                  *reinterpret_cast<uint4*>(out + e) =
-                      make_uint4(pack2<kBf16>(o[e] * inv, o[e + 1] * inv), pack2<kBf16>(o[e + 2] * inv, o[e + 3] * inv),
-                                 pack2<kBf16>(o[e + 4] * inv, o[e + 5] * inv), pack2<kBf16>(o[e + 6] * inv, o[e + 7] * inv));
+              for (int e = 0; e < 8; ++e) y[e] = pack2<kBf16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+              uint16_t* out = static_cast<uint16_t*>(P.out) + (static_cast<int64_t>(row) * P.Hq + head) * P.D + c;
+              *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
+              if (c + 8 < P.D) *reinterpret_cast<uint4*>(out + 8) = make_uint4(y[4], y[5], y[6], y[7]);
             } else {
               float4* po = reinterpret_cast<float4*>(P.part_o) +
                            (static_cast<int64_t>(slot * 2 + (join ? 0 : wg)) * (DP / 4) + c / 4) * kTile + r;
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) po[(e / 4) * kTile] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 16; e += 4) po[(e / 4) * kTile] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
         }
@@ -814,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     if (tid == 0) {
       // for the join: the cut unit's first node, nodes, key head, slot; parts behind this one
-      const int more = cut ? static_cast<int>((cut_left + chunk - 1) / chunk) : 0;
+      const int more = cut ? static_cast<int>((cut_left + sh.chunk - 1) / sh.chunk) : 0;
       P.desc[cta * 2] = cut ? cut_at : make_int4(0, 0, 0, 0);
       P.desc[cta * 2 + 1] = make_int4(more, 0, 0, 0);
     }
@@ -823,8 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   __syncthreads();
   tc_fence_after();
   if (sh.dead) {  // a wait ran out: NaN for every row of this CTA's parts
-    Walk k{};
-    if (begin < total) k = sh.start;
+    Walk k = sh.start;
     for (int seg = 0; k.next(P); ++seg) {
       const bool whole = k.j0 == 0 && k.j1 == k.s.J;
       const int slot = cta * 2 + (seg == 0 ? 0 : 1), from = k.u * 2 * P.npt;
@@ -842,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       if (tid == 0) {
         const bool cut = k.j0 == 0 && k.j1 < k.s.J;
         P.desc[cta * 2] = cut ? make_int4(k.s.lo + from, min(k.s.n - from, 2 * P.npt), k.h, slot) : make_int4(0, 0, 0, 0);
-        P.desc[cta * 2 + 1] = make_int4(cut ? static_cast<int>((k.s.J - k.j1 + chunk - 1) / chunk) : 0, 0, 0, 0);
+        P.desc[cta * 2 + 1] = make_int4(cut ? static_cast<int>((k.s.J - k.j1 + sh.chunk - 1) / sh.chunk) : 0, 0, 0, 0);
       }
     }
   }
@@ -859,6 +879,8 @@ constexpr int kJoinThreads = 256;
 template <int DP, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ AttnParams P) {
   __shared__ int first[kJoinThreads];   // first item behind each unit
+  __shared__ int4 unit[kMaxCtas];
+  __shared__ int parts_s[kMaxCtas];
   __shared__ int wsum[8];
   __shared__ float4 acc_s[8][32];
   __shared__ float2 st_s[8][32];
@@ -867,9 +889,12 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int items = 0;
   if (tid < P.ctas) {
-    const int nodes = P.desc[tid * 2].y, more = P.desc[tid * 2 + 1].x;
-    const int blocks = nodes == 0 ? 0 : nodes > P.npt ? 4 + cdiv((nodes - P.npt) * P.G, 32) : cdiv(nodes * P.G, 32);
-    items = blocks * (more + 1 >= 8 ? DP / 4 : DP / 32);
+    const int4 d = P.desc[tid * 2];
+    const int parts = P.desc[tid * 2 + 1].x + 1;
+    unit[tid] = d;
+    parts_s[tid] = parts;
+    const int blocks = d.y == 0 ? 0 : d.y > P.npt ? 4 + cdiv((d.y - P.npt) * P.G, 32) : cdiv(d.y * P.G, 32);
+    items = blocks * (parts >= 8 ? DP / 4 : DP / 32);
   }
   int incl = items;
 #pragma unroll
@@ -894,8 +919,8 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
       }
     }
     const int cta = lo;
-    const int4 d = P.desc[cta * 2];
-    const int parts = P.desc[cta * 2 + 1].x + 1;
+    const int4 d = unit[cta];
+    const int parts = parts_s[cta];
     const int k = item - (cta > 0 ? first[cta - 1] : 0);
     const bool split = parts >= 8;
     const int cgs = split ? DP / 4 : DP / 32;
@@ -907,19 +932,34 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
     float top = -INFINITY, sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (mine) {
-      const int p0 = split ? warp : 0, step = split ? 8 : 1;
-#pragma unroll 4
-      for (int p = p0; p < parts; p += step) top = fmaxf(top, P.part_s[at(p) * kTile + r].x);
-#pragma unroll 4
-      for (int p = p0; p < parts; p += step) {
-        const float2 s = P.part_s[at(p) * kTile + r];
-        const float4 x = reinterpret_cast<const float4*>(P.part_o)[(at(p) * (DP / 4) + cg) * kTile + r];
-        const float f = s.x == -INFINITY ? 0.0f : ex2_approx(s.x - top);
-        sum += f * s.y;
-        o.x += f * x.x;
-        o.y += f * x.y;
-        o.z += f * x.z;
-        o.w += f * x.w;
+      // four parts at a time, loaded together; the shift follows the largest so far
+      const int step = split ? 8 : 1;
+      for (int p = split ? warp : 0; p < parts; p += 4 * step) {
+        float2 s[4];
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[i] = make_float2(-INFINITY, 0.0f);
+          x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (p + i * step < parts) {
+            s[i] = P.part_s[at(p + i * step) * kTile + r];
+            x[i] = reinterpret_cast<const float4*>(P.part_o)[(at(p + i * step) * (DP / 4) + cg) * kTile + r];
+          }
+        }
+        const float now = fmaxf(top, fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x)));
+        const float g = top == -INFINITY ? 0.0f : ex2_approx(top - now);
+        top = now;
+        sum *= g;
+        o = make_float4(o.x * g, o.y * g, o.z * g, o.w * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = s[i].x == -INFINITY ? 0.0f : ex2_approx(s[i].x - top);
+          sum += f * s[i].y;
+          o.x += f * x[i].x;
+          o.y += f * x[i].y;
+          o.z += f * x[i].z;
+          o.w += f * x[i].w;
+        }
       }
     }
     if (split) {
@@ -992,8 +1032,6 @@ int make_map(EncodeFn enc, CUtensorMap* map, bool bf16, const void* base, int ra
   if (r != CUDA_SUCCESS) return set_error(SV_ERR_INVALID_ARG, "%s: layout not accepted (driver status %d)", what, static_cast<int>(r));
   return SV_OK;
 }
-
-constexpr int kMaxCtas = 160;  // SMs of a device, with room
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
