@@ -58,52 +58,62 @@ def _lib():
     return L
 
 
-def _same_device(first, **rest):
-    if not first.is_cuda:
+# The argument checks run on every call of a serving step, some of which take
+# a few microseconds on the device: one comparison each, details on failure.
+def _same_device(first, *rest):
+    dev = first.device
+    if dev.type != "cuda":
         raise ValueError("tensors must be CUDA tensors (no CPU path)")
-    for name, t in rest.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+    return dev
 
 
-def _want(t, name, dtype, *shape, contiguous=True):
-    """Shape, type and contiguity of one argument; None in `shape` matches any size."""
-    if t.dtype != dtype or t.dim() != len(shape) or any(
-            s is not None and s != n for s, n in zip(shape, t.shape)):
-        want = ", ".join("*" if s is None else str(s) for s in shape)
-        raise ValueError(f"{name} must be {str(dtype).removeprefix('torch.')} [{want}], got "
-                         f"{str(t.dtype).removeprefix('torch.')} {list(t.shape)}")
-    if contiguous and not t.is_contiguous():
+def _dims(t, name, n):
+    """The shape of an argument that must have n axes."""
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} axes, got {list(shape)}")
+    return shape
+
+
+def _want(t, name, dtype, shape, dense=True):
+    """Type, shape and (dense) contiguity of one argument."""
+    if t.dtype is dtype and t.shape == shape and (not dense or t.is_contiguous()):
+        return
+    if t.dtype is dtype and t.shape == shape:
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be {str(dtype).removeprefix('torch.')} {list(shape)}, got "
+                     f"{str(t.dtype).removeprefix('torch.')} {list(t.shape)}")
+
+
+def _rows(table, B, W):
+    if B > 0 and W > 1 and table.stride(1) != 1:
+        raise ValueError("block_table rows must be contiguous")
 
 
 def _p(t):
     return None if t is None or t.numel() == 0 else t.data_ptr()
 
 
-class _Call:
-    """The device, the stream and the allocations of one call: outputs and
-    scratch space are allocated on the stream that the kernels run on."""
-
-    def __init__(self, device, stream):
-        self._dev = _on(device)
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self._ctx = torch.cuda.stream(self.stream)
-
-    def __enter__(self):
-        self._dev.__enter__()
-        self._ctx.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        self._ctx.__exit__(*exc)
-        self._dev.__exit__(*exc)
+def _call(device, stream, body):
+    """body(stream handle) with the tensors' device current and with the
+    stream that the kernels run on current too, since that is where outputs and
+    scratch space are allocated."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return body(torch.cuda.current_stream(device).cuda_stream)
+    with _on(device):
+        if stream is None:
+            return body(torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.stream(stream):
+            return body(stream.cuda_stream)
 
 
 def _out(t, name, dtype, shape, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _want(t, name, dtype, *shape)
+    _want(t, name, dtype, shape)
     return t
 
 
@@ -115,24 +125,25 @@ def spec_verify_probs(target, draft, tokens, uniforms, draw_uniforms, *, out_acc
     Token x at position i is accepted when u q(x) < p(x); the first rejection's
     correction token is drawn from max(p - q, 0) by draw_uniforms, the bonus
     token from target row g.  Returns (accept_len [B], tokens [B, g+1])."""
-    _same_device(target, draft=draft, tokens=tokens, uniforms=uniforms,
-                 draw_uniforms=draw_uniforms, out_accept_len=out_accept_len,
-                 out_tokens=out_tokens)
+    dev = _same_device(target, draft, tokens, uniforms, draw_uniforms, out_accept_len, out_tokens)
     dt = _dt(target)
-    _want(target, "target", target.dtype, None, None, None)
-    B, g1, V = target.shape
+    B, g1, V = _dims(target, "target", 3)
+    g = g1 - 1
+    _want(target, "target", target.dtype, (B, g1, V))
     if draft is not None:
-        _want(draft, "draft", target.dtype, B, g1 - 1, V)
-    _want(tokens, "tokens", torch.int32, B, g1 - 1)
-    _want(uniforms, "uniforms", torch.float32, B, g1 - 1)
-    _want(draw_uniforms, "draw_uniforms", torch.float32, B)
-    dev = target.device
-    with _Call(dev, stream) as s:
+        _want(draft, "draft", target.dtype, (B, g, V))
+    _want(tokens, "tokens", torch.int32, (B, g))
+    _want(uniforms, "uniforms", torch.float32, (B, g))
+    _want(draw_uniforms, "draw_uniforms", torch.float32, (B,))
+
+    def body(s):
         acc = _out(out_accept_len, "out_accept_len", torch.int32, (B,), dev)
         tok = _out(out_tokens, "out_tokens", torch.int32, (B, g1), dev)
         _check(_lib().spec_verify_probs(_p(target), _p(draft), _p(tokens), _p(uniforms),
-                                        _p(draw_uniforms), B, g1 - 1, V, dt, _p(acc), _p(tok), s))
-    return acc, tok
+                                        _p(draw_uniforms), B, g, V, dt, _p(acc), _p(tok), s))
+        return acc, tok
+
+    return _call(dev, stream, body)
 
 
 def spec_verify_tree(target, draft, tokens, parents, cu_nodes, uniforms, draw_uniforms, *,
@@ -145,29 +156,30 @@ def spec_verify_tree(target, draft, tokens, parents, cu_nodes, uniforms, draw_un
     were drawn from (None for point drafts); tokens [N] int32, uniforms [N],
     draw_uniforms [B] fp32; max_nodes: the most nodes a sequence has.
     Returns (accept_len [B], tokens [B, max_nodes], path [B, max_nodes])."""
-    _same_device(target, draft=draft, tokens=tokens, parents=parents, cu_nodes=cu_nodes,
-                 uniforms=uniforms, draw_uniforms=draw_uniforms, out_accept_len=out_accept_len,
-                 out_tokens=out_tokens, out_path=out_path)
+    dev = _same_device(target, draft, tokens, parents, cu_nodes, uniforms, draw_uniforms,
+                       out_accept_len, out_tokens, out_path)
     dt = _dt(target)
-    _want(target, "target", target.dtype, None, None)
-    N, V = target.shape
+    N, V = _dims(target, "target", 2)
+    B, = _dims(draw_uniforms, "draw_uniforms", 1)
+    _want(target, "target", target.dtype, (N, V))
     if draft is not None:
-        _want(draft, "draft", target.dtype, N, V)
-    for t, n in ((tokens, "tokens"), (parents, "parents")):
-        _want(t, n, torch.int32, N)
-    _want(uniforms, "uniforms", torch.float32, N)
-    _want(draw_uniforms, "draw_uniforms", torch.float32, None)
-    B = draw_uniforms.shape[0]
-    _want(cu_nodes, "cu_nodes", torch.int32, B + 1)
-    dev = target.device
-    with _Call(dev, stream) as s:
+        _want(draft, "draft", target.dtype, (N, V))
+    _want(tokens, "tokens", torch.int32, (N,))
+    _want(parents, "parents", torch.int32, (N,))
+    _want(uniforms, "uniforms", torch.float32, (N,))
+    _want(draw_uniforms, "draw_uniforms", torch.float32, (B,))
+    _want(cu_nodes, "cu_nodes", torch.int32, (B + 1,))
+
+    def body(s):
         acc = _out(out_accept_len, "out_accept_len", torch.int32, (B,), dev)
         tok = _out(out_tokens, "out_tokens", torch.int32, (B, max_nodes), dev)
         path = _out(out_path, "out_path", torch.int32, (B, max_nodes), dev)
         _check(_lib().spec_verify_tree(_p(target), _p(draft), _p(tokens), _p(parents),
                                        _p(cu_nodes), _p(uniforms), _p(draw_uniforms), B, N,
                                        max_nodes, V, dt, _p(acc), _p(tok), _p(path), s))
-    return acc, tok, path
+        return acc, tok, path
+
+    return _call(dev, stream, body)
 
 
 def kv_slots(lens, add, cu_rows, block_table, free_pages, free_count, *, rows: int,
@@ -182,33 +194,34 @@ def kv_slots(lens, add, cu_rows, block_table, free_pages, free_count, *, rows: i
     free_count [1]); slots is -1 for rows not kept, start -1 for a request that
     was refused (no pages, table row too short) or released.  out_lens and
     out_free_count may be lens and free_count."""
-    _same_device(lens, add=add, cu_rows=cu_rows, block_table=block_table, free_pages=free_pages,
-                 free_count=free_count, path=path, out_slots=out_slots, out_start=out_start,
-                 out_lens=out_lens, out_free_count=out_free_count)
-    _want(lens, "lens", torch.int32, None)
-    B = lens.shape[0]
-    _want(add, "add", torch.int32, B)
-    _want(cu_rows, "cu_rows", torch.int32, B + 1)
-    _want(block_table, "block_table", torch.int32, B, None, contiguous=False)
-    W = block_table.shape[1]
-    if B > 0 and W > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table rows must be contiguous")
-    _want(free_pages, "free_pages", torch.int32, None)
-    _want(free_count, "free_count", torch.int32, 1)
+    dev = _same_device(lens, add, cu_rows, block_table, free_pages, free_count, path, out_slots,
+                       out_start, out_lens, out_free_count)
+    B, = _dims(lens, "lens", 1)
+    W = _dims(block_table, "block_table", 2)[1]
+    pool, = _dims(free_pages, "free_pages", 1)
+    width = 0 if path is None else _dims(path, "path", 2)[1]
+    _want(lens, "lens", torch.int32, (B,))
+    _want(add, "add", torch.int32, (B,))
+    _want(cu_rows, "cu_rows", torch.int32, (B + 1,))
+    _want(block_table, "block_table", torch.int32, (B, W), dense=False)
+    _rows(block_table, B, W)
+    _want(free_pages, "free_pages", torch.int32, (pool,))
+    _want(free_count, "free_count", torch.int32, (1,))
     if path is not None:
-        _want(path, "path", torch.int32, B, None)
-    dev = lens.device
-    with _Call(dev, stream) as s:
+        _want(path, "path", torch.int32, (B, width))
+
+    def body(s):
         slots = _out(out_slots, "out_slots", torch.int32, (rows,), dev)
         start = _out(out_start, "out_start", torch.int32, (B,), dev)
         new = _out(out_lens, "out_lens", torch.int32, (B,), dev)
         count = _out(out_free_count, "out_free_count", torch.int32, (1,), dev)
         _check(_lib().spec_kv_slots(
-            _p(lens), _p(add), _p(cu_rows), _p(path), 0 if path is None else path.shape[1],
-            _p(block_table), block_table.stride(0) if B > 1 else W, W, _p(free_pages),
-            free_pages.shape[0], _p(free_count), B, rows, page_size, _p(slots), _p(start), _p(new),
-            _p(count), s))
-    return slots, start, new, count
+            _p(lens), _p(add), _p(cu_rows), _p(path), width, _p(block_table),
+            block_table.stride(0) if B > 1 else W, W, _p(free_pages), pool, _p(free_count), B,
+            rows, page_size, _p(slots), _p(start), _p(new), _p(count), s))
+        return slots, start, new, count
+
+    return _call(dev, stream, body)
 
 
 def kv_append(k, v, slots, k_cache, v_cache, *, stream=None):
@@ -217,34 +230,34 @@ def kv_append(k, v, slots, k_cache, v_cache, *, stream=None):
     D]; slots (int32) outside the cache skip the row.  With a leading layer
     axis on all four, every layer at once.  Strides are free but for the last
     axis; k, v must not overlap the caches.  Returns None."""
-    _same_device(k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache)
-    if k.dim() not in (3, 4):
-        raise ValueError(f"k must be [N, H, D] or [layers, N, H, D], got {list(k.shape)}")
-    lead = tuple(k.shape[:k.dim() - 3])
-    N, H, D = k.shape[-3:]
-    _want(v, "v", k.dtype, *lead, N, H, D, contiguous=False)
-    _want(k_cache, "k_cache", k.dtype, *lead, None, None, H, D, contiguous=False)
-    pages, page = k_cache.shape[-4:-2]
-    _want(v_cache, "v_cache", k.dtype, *lead, pages, page, H, D, contiguous=False)
-    _want(slots, "slots", torch.int32, N)
+    dev = _same_device(k, v, slots, k_cache, v_cache)
+    shape = k.shape
+    if len(shape) not in (3, 4):
+        raise ValueError(f"k must be [N, H, D] or [layers, N, H, D], got {list(shape)}")
+    lead = tuple(shape[:-3])
+    N, H, D = shape[-3:]
+    pages, page = _dims(k_cache, "k_cache", len(shape) + 1)[-4:-2]
+    _want(v, "v", k.dtype, shape, dense=False)
+    _want(k_cache, "k_cache", k.dtype, lead + (pages, page, H, D), dense=False)
+    _want(v_cache, "v_cache", k.dtype, lead + (pages, page, H, D), dense=False)
+    _want(slots, "slots", torch.int32, (N,))
     es = k.element_size()
     if es not in (1, 2, 4):
         raise ValueError(f"elements of 1, 2 or 4 bytes are copied, got {k.dtype}")
-    for t, n in ((k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache")):
-        if D > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{n}'s last axis must be contiguous")
-    if N == 0 or H == 0 or D == 0 or pages == 0 or page == 0 or 0 in lead:
+    if k.numel() == 0 or k_cache.numel() == 0:
         return
-    a = _AppendArgs(slots=_p(slots), layers=lead[0] if lead else 1, N=N, H=H, D=D,
-                    num_pages=pages, page_size=page, elem_bytes=es)
-    for w, (x, cache) in enumerate(((k, k_cache), (v, v_cache))):
-        a.src[w], a.cache[w] = x.data_ptr(), cache.data_ptr()
-        a.src_layer[w] = x.stride(0) if lead else 0
-        a.cache_layer[w] = cache.stride(0) if lead else 0
-        a.src_row[w], a.src_head[w] = x.stride(-3), x.stride(-2)
-        a.cache_page[w], a.cache_token[w], a.cache_head[w] = cache.stride()[-4:-1]
-    with _Call(k.device, stream) as s:
-        _check(_lib().spec_kv_append(C.byref(a), s))
+    ks, vs, kcs, vcs = k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
+    if D > 1 and not ks[-1] == vs[-1] == kcs[-1] == vcs[-1] == 1:
+        raise ValueError("the last axis of k, v and the caches must be contiguous")
+    two = _i64 * 2
+    layered = bool(lead)
+    a = _AppendArgs(
+        (_vp * 2)(k.data_ptr(), v.data_ptr()), (_vp * 2)(k_cache.data_ptr(), v_cache.data_ptr()),
+        two(ks[0], vs[0]) if layered else two(), two(ks[-3], vs[-3]), two(ks[-2], vs[-2]),
+        two(kcs[0], vcs[0]) if layered else two(), two(kcs[-4], vcs[-4]), two(kcs[-3], vcs[-3]),
+        two(kcs[-2], vcs[-2]), slots.data_ptr(), lead[0] if layered else 1, N, H, D, pages, page,
+        es)
+    _call(dev, stream, lambda s: _check(_lib().spec_kv_append(C.byref(a), s)))
 
 
 def tree_attention_workspace_size(Hq: int, Hkv: int, D: int) -> int:
@@ -263,44 +276,46 @@ def tree_attention(q, k, v, k_cache, v_cache, block_table, lens, parents, cu_nod
     defaults to D ** -0.5.  Returns (out [N, Hq, D], lse [N, Hq] fp32 or
     None).  `workspace`: a uint8 tensor of tree_attention_workspace_size
     bytes, of any content; calls that may run at once need one each."""
-    _same_device(q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                 lens=lens, parents=parents, cu_nodes=cu_nodes, out=out, out_lse=out_lse,
-                 workspace=workspace)
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    _want(q, "q", q.dtype, None, None, None, contiguous=False)
-    N, Hq, D = q.shape
-    _want(k, "k", q.dtype, N, None, D, contiguous=False)
-    Hkv = k.shape[1]
-    _want(v, "v", q.dtype, N, Hkv, D, contiguous=False)
-    _want(k_cache, "k_cache", q.dtype, None, None, Hkv, D, contiguous=False)
-    pages, page = k_cache.shape[:2]
-    _want(v_cache, "v_cache", q.dtype, pages, page, Hkv, D, contiguous=False)
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.stride(-1) != 1 and t.numel() > 0:
-            raise ValueError(f"{n}'s last axis must be contiguous")
-    _want(lens, "lens", torch.int32, None)
-    B = lens.shape[0]
-    _want(cu_nodes, "cu_nodes", torch.int32, B + 1)
-    _want(parents, "parents", torch.int32, N)
-    _want(block_table, "block_table", torch.int32, B, None, contiguous=False)
-    W = block_table.shape[1]
-    if B > 0 and W > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table rows must be contiguous")
-    dev = q.device
-    with _Call(dev, stream) as s:
-        out = _out(out, "out", q.dtype, (N, Hq, D), dev)
-        if with_lse or out_lse is not None:
-            out_lse = _out(out_lse, "out_lse", torch.float32, (N, Hq), dev)
-        if workspace is None:
-            workspace = torch.empty(max(tree_attention_workspace_size(Hq, Hkv, D), 256),
-                                    dtype=torch.uint8, device=dev)
+    dev = _same_device(q, k, v, k_cache, v_cache, block_table, lens, parents, cu_nodes, out,
+                       out_lse, workspace)
+    dt = q.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise TypeError(f"q must be bfloat16 or float16, got {dt}")
+    N, Hq, D = _dims(q, "q", 3)
+    Hkv = _dims(k, "k", 3)[1]
+    pages, page = _dims(k_cache, "k_cache", 4)[:2]
+    B, = _dims(lens, "lens", 1)
+    W = _dims(block_table, "block_table", 2)[1]
+    _want(k, "k", dt, (N, Hkv, D), dense=False)
+    _want(v, "v", dt, (N, Hkv, D), dense=False)
+    _want(k_cache, "k_cache", dt, (pages, page, Hkv, D), dense=False)
+    _want(v_cache, "v_cache", dt, (pages, page, Hkv, D), dense=False)
+    _want(lens, "lens", torch.int32, (B,))
+    _want(cu_nodes, "cu_nodes", torch.int32, (B + 1,))
+    _want(parents, "parents", torch.int32, (N,))
+    _want(block_table, "block_table", torch.int32, (B, W), dense=False)
+    _rows(block_table, B, W)
+    qs, ks, vs, kcs, vcs = q.stride(), k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
+    if N > 0 and not qs[2] == ks[2] == vs[2] == kcs[3] == vcs[3] == 1:
+        raise ValueError("the last axis of q, k, v and the caches must be contiguous")
+
+    def body(s):
+        o = _out(out, "out", dt, (N, Hq, D), dev)
+        lse = out_lse
+        if with_lse or lse is not None:
+            lse = _out(lse, "out_lse", torch.float32, (N, Hq), dev)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(max(tree_attention_workspace_size(Hq, Hkv, D), 256),
+                             dtype=torch.uint8, device=dev)
         a = _AttentionArgs(
-            _p(q), _p(k), _p(v), _p(k_cache), _p(v_cache), _p(out), _p(out_lse),
-            _p(block_table), _p(lens), _p(parents), _p(cu_nodes), *q.stride()[:2],
-            *k.stride()[:2], *v.stride()[:2], *k_cache.stride()[:3], *v_cache.stride()[:3],
-            block_table.stride(0), B, N, Hq, Hkv, D, pages, page, W,
-            1 if q.dtype == torch.bfloat16 else F16, D ** -0.5 if scale is None else scale)
-        _check(_lib().spec_tree_attention(C.byref(a), workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), s))
-    return out, out_lse
+            _p(q), _p(k), _p(v), _p(k_cache), _p(v_cache), _p(o), _p(lse), _p(block_table),
+            _p(lens), _p(parents), _p(cu_nodes), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], kcs[0],
+            kcs[1], kcs[2], vcs[0], vcs[1], vcs[2], block_table.stride(0), B, N, Hq, Hkv, D,
+            pages, page, W, 1 if dt is torch.bfloat16 else F16,
+            D ** -0.5 if scale is None else scale)
+        _check(_lib().spec_tree_attention(C.byref(a), ws.data_ptr(),
+                                          ws.numel() * ws.element_size(), s))
+        return o, lse
+
+    return _call(dev, stream, body)
