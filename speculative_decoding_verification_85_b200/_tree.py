@@ -94,7 +94,7 @@ def _rows(table, B, W):
 
 
 def _p(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return None if t is None else t.data_ptr()
 
 
 def _call(device, stream, body):

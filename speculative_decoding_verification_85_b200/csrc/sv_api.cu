@@ -5,6 +5,8 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <set>
+#include <utility>
 
 #include "spec_verify.h"
 #include "spec_verify_shard.h"
@@ -58,6 +60,22 @@ int check_device() {
     if (cached[dev] == 2)
       return set_error(SV_ERR_UNSUPPORTED, "device %d is not sm_100 (this library is built for sm_100a)", dev);
   }
+  return SV_OK;
+}
+
+int allow_kernel(const void* kernel, size_t smem, bool large_clusters) {
+  static std::mutex mu;
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  std::lock_guard<std::mutex> lk(mu);
+  if (done.count({dev, kernel})) return SV_OK;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess && large_clusters)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  done.insert({dev, kernel});
   return SV_OK;
 }
 

@@ -1073,12 +1073,10 @@ template <int DP, bool kBf16>
 int launch_attn(const AttnParams& p, int ctas, cudaStream_t stream) {
   constexpr size_t kSmem = Shape<DP>::kTiles + sizeof(Shared);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<DP, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmem));
-  if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-  attn_kernel<DP, kBf16><<<ctas, kThreads, kSmem, stream>>>(p);
-  int rc = check_launch("tree attention");
+  int rc = allow_kernel(reinterpret_cast<const void*>(attn_kernel<DP, kBf16>), kSmem, false);
   if (rc != SV_OK) return rc;
+  attn_kernel<DP, kBf16><<<ctas, kThreads, kSmem, stream>>>(p);
+  if ((rc = check_launch("tree attention")) != SV_OK) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas * 4);
   cfg.blockDim = dim3(kJoinThreads);
@@ -1088,7 +1086,7 @@ int launch_attn(const AttnParams& p, int ctas, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, combine_kernel<DP, kBf16>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, combine_kernel<DP, kBf16>, p);
   if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "tree attention join launch: %s", cudaGetErrorString(e));
   return SV_OK;
 }

@@ -14,6 +14,7 @@ namespace {
 
 // ------------------------------------------------------------------- slots
 constexpr int kSThreads = 1024;
+constexpr int kRowsCached = 4096;  // requests whose row bounds a block keeps on chip
 
 struct SlotParams {
   const int32_t *lens, *add, *cu, *path;
@@ -99,19 +100,23 @@ __device__ __forceinline__ int owner_of(const int64_t* incl, int n, int64_t k) {
   return lo;
 }
 
-// Slot of one packed row, -1 when it is not kept.
-__device__ __forceinline__ int slot_of(const SlotParams& P, int row) {
-  if (P.B == 0) return -1;
-  int lo = 0, hi = P.B - 1;  // last request whose rows start at or before `row`
+// The last request whose rows start at or before `row`.
+__device__ __forceinline__ int request_at(const int32_t* cu, int B, int row) {
+  int lo = 0, hi = B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (P.cu[mid] <= row) {
+    if (cu[mid] <= row) {
       lo = mid;
     } else {
       hi = mid - 1;
     }
   }
-  const int b = lo, first = P.cu[b];
+  return lo;
+}
+
+// Slot of row `row` if it belongs to request b, -1 when it is not kept.
+__device__ __forceinline__ int slot_of(const SlotParams& P, int b, int row) {
+  const int first = P.cu[b];
   if (row < first || row >= P.cu[b + 1]) return -1;
   const int begin = P.start[b];
   if (begin < 0) return -1;
@@ -132,11 +137,16 @@ __device__ __forceinline__ int slot_of(const SlotParams& P, int row) {
   return page < 0 || slot > INT_MAX ? -1 : static_cast<int>(slot);
 }
 
-// One block: the requests' prefix sums decide who grows and which free pages
-// it takes; the pages are handed out flat over the threads (a long prompt
-// takes thousands).  The rows' slots follow in the same launch when there are
-// few of them (kRowsHere), else slots_rows_kernel does them.
-template <bool kRowsHere>
+// The requests' prefix sums decide who grows and which free pages it takes;
+// the pages are handed out flat over the threads (a long prompt takes
+// thousands).  Bound by latency: one block does it all, slots included, when
+// there are few rows.  For many, a cluster of kSlotCtas blocks shares out the
+// pages (every block runs the same sums; the first one writes the requests'
+// outputs, which may be their inputs, once all have read), and
+// slots_rows_kernel does the rows: 512 prompts, 10^6 rows and 66,000 pages
+// took 67 us with one block.
+constexpr int kSlotCtas = 8;
+template <bool kMany>
 __global__ void __launch_bounds__(kSThreads) slots_kernel(const SlotParams P) {
   __shared__ int64_t warps[32];
   __shared__ int64_t incl_s[kSThreads];
@@ -144,6 +154,15 @@ __global__ void __launch_bounds__(kSThreads) slots_kernel(const SlotParams P) {
   __shared__ int64_t popped_s;
   __shared__ int release_s;
   const int tid = threadIdx.x;
+  const int rank = kMany ? blockIdx.x : 0, ctas = kMany ? kSlotCtas : 1;
+  auto sync = [&]() {
+    if constexpr (kMany) {
+      asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+  };
   const int64_t count = min(max(*P.free_count, 0), P.pool);
   if (tid == 0) {
     popped_s = 0;
@@ -162,25 +181,28 @@ __global__ void __launch_bounds__(kSThreads) slots_kernel(const SlotParams P) {
     incl_s[tid] = incl;
     have_s[tid] = q.have;
     need_s[tid] = q.need;
-    if (r < P.B) {
-      P.start[r] = ok ? q.len : -1;
-      if (!q.release) P.out_lens[r] = ok ? q.len + q.add : q.len;
-      if (q.release) release_s = 1;
-    }
+    if (q.release) release_s = 1;
     // the largest prefix that still fits (a later one never does)
     if (ok && q.need) atomicMax(reinterpret_cast<unsigned long long*>(&popped_s), static_cast<unsigned long long>(incl));
-    __syncthreads();
+    sync();
+    if (r < P.B && rank == 0) {
+      P.start[r] = ok ? q.len : -1;
+      if (!q.release) P.out_lens[r] = ok ? q.len + q.add : q.len;
+    }
     const int64_t popped = popped_s;
-    for (int64_t k = carry + tid; k < popped; k += kSThreads) {
+#pragma unroll 4
+    for (int64_t k = carry + rank * kSThreads + tid; k < popped; k += ctas * kSThreads) {
       const int o = owner_of(incl_s, kSThreads, k);
       const int64_t nth = k - (incl_s[o] - need_s[o]);
-      P.table[(base + o) * P.table_row + have_s[o] + nth] = P.free_pages[count - 1 - k];
+      P.table[(base + o) * P.table_row + have_s[o] + nth] = __ldcg(P.free_pages + (count - 1 - k));
     }
     carry += total;
     __syncthreads();
   }
 
   int64_t top = count - popped_s;
+  sync();  // pages on the stack are overwritten only now
+  if (rank != 0) return;
   if (release_s) {  // the pages of released requests go on top of what is left
     for (int base = 0; base < P.B; base += kSThreads) {
       const int r = base + tid;
@@ -202,15 +224,37 @@ __global__ void __launch_bounds__(kSThreads) slots_kernel(const SlotParams P) {
     }
   }
   if (tid == 0) *P.out_count = static_cast<int>(min(top, static_cast<int64_t>(P.pool)));
-  if constexpr (kRowsHere) {
+  if constexpr (!kMany) {
     __syncthreads();
-    for (int row = tid; row < P.N; row += kSThreads) P.slots[row] = slot_of(P, row);
+    for (int row = tid; row < P.N; row += kSThreads) P.slots[row] = P.B ? slot_of(P, request_at(P.cu, P.B, row), row) : -1;
   }
 }
 
+// Four consecutive rows a thread: one search, then forward from there.
 __global__ void __launch_bounds__(256) slots_rows_kernel(const SlotParams P) {
-  const int row = blockIdx.x * 256 + threadIdx.x;
-  if (row < P.N) P.slots[row] = slot_of(P, row);
+  __shared__ int32_t bounds[kRowsCached];
+  const bool cached = P.B <= kRowsCached;
+  if (cached)
+    for (int i = threadIdx.x; i < P.B; i += 256) bounds[i] = P.cu[i];
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (row0 >= P.N) return;
+  int b = P.B ? request_at(cached ? bounds : P.cu, P.B, static_cast<int>(row0)) : 0;
+  int y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = static_cast<int>(min(row0 + i, static_cast<int64_t>(P.N) - 1));
+    while (b + 1 < P.B && P.cu[b + 1] <= row) ++b;
+    y[i] = P.B ? slot_of(P, b, row) : -1;
+  }
+  if (row0 + 4 <= P.N && reinterpret_cast<uintptr_t>(P.slots) % 16 == 0) {
+    *reinterpret_cast<int4*>(P.slots + row0) = make_int4(y[0], y[1], y[2], y[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row0 + i < P.N) P.slots[row0 + i] = y[i];
+  }
 }
 
 // ------------------------------------------------------------------ append
@@ -295,13 +339,27 @@ int spec_kv_slots(const int32_t* lens, const int32_t* add, const int32_t* cu_row
                out_lens, out_free_count, table_row, path_width, table_width, pool, B, N, page_size};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (N <= 8 * kSThreads) {
-    slots_kernel<true><<<1, kSThreads, 0, s>>>(p);
+    slots_kernel<false><<<1, kSThreads, 0, s>>>(p);
     return check_launch("slots");
   }
-  slots_kernel<false><<<1, kSThreads, 0, s>>>(p);
-  if ((rc = check_launch("slots")) != SV_OK) return rc;
-  slots_rows_kernel<<<(N + 255) / 256, 256, 0, s>>>(p);
-  return check_launch("slots rows");
+  cudaLaunchAttribute at[1];
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kSlotCtas);
+  cfg.blockDim = dim3(kSThreads);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {kSlotCtas, 1, 1};
+  cudaError_t e = cudaLaunchKernelEx(&cfg, slots_kernel<true>, p);
+  if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "slots launch: %s", cudaGetErrorString(e));
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(N) + 1023) / 1024));
+  cfg.blockDim = dim3(256);
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  e = cudaLaunchKernelEx(&cfg, slots_rows_kernel, p);
+  if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "slots rows launch: %s", cudaGetErrorString(e));
+  return SV_OK;
 }
 
 int spec_kv_append(const sv_kv_append_args* a, void* stream) {

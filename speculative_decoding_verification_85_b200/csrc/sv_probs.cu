@@ -457,11 +457,8 @@ int launch_probs(ProbsParams p, int B, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(p.chunks) * sizeof(double) + static_cast<size_t>(cap) * 7 * 4;
   if (smem > kMaxSmem)
     return set_error(SV_ERR_UNSUPPORTED, "V = %d is too large for B = %d", p.V, B);
-  cudaError_t e = cudaFuncSetAttribute(probs_kernel<kBf16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(probs_kernel<kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kMaxSmem));
-  if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  const int rc = allow_kernel(reinterpret_cast<const void*>(probs_kernel<kBf16>), kMaxSmem, true);
+  if (rc != SV_OK) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(B) * C);
   cfg.blockDim = dim3(kPThreads);
@@ -472,7 +469,7 @@ int launch_probs(ProbsParams p, int B, cudaStream_t stream) {
   at[0].val.clusterDim = {static_cast<unsigned>(C), 1, 1};
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, probs_kernel<kBf16>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, probs_kernel<kBf16>, p);
   if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "probs launch: %s", cudaGetErrorString(e));
   return SV_OK;
 }
