@@ -12,6 +12,9 @@ F16 = 2
 MAX_NODES = 1024
 
 _vp, _i32, _i64 = C.c_void_p, C.c_int, C.c_int64
+# the current stream's handle, without an object around it where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _AppendArgs(C.Structure):
@@ -59,15 +62,12 @@ def _lib():
 
 
 # The argument checks run on every call of a serving step, some of which take
-# a few microseconds on the device: one comparison each, details on failure.
-def _same_device(first, *rest):
-    dev = first.device
-    if dev.type != "cuda":
+# a few microseconds on the device: one pass over (tensor, name, type, shape,
+# dense) rows, details on failure.
+def _device(t):
+    if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors (no CPU path)")
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
-    return dev
+    return t.device
 
 
 def _dims(t, name, n):
@@ -78,14 +78,17 @@ def _dims(t, name, n):
     return shape
 
 
-def _want(t, name, dtype, shape, dense=True):
-    """Type, shape and (dense) contiguity of one argument."""
-    if t.dtype is dtype and t.shape == shape and (not dense or t.is_contiguous()):
-        return
-    if t.dtype is dtype and t.shape == shape:
-        raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} must be {str(dtype).removeprefix('torch.')} {list(shape)}, got "
-                     f"{str(t.dtype).removeprefix('torch.')} {list(t.shape)}")
+def _want(device, *checks):
+    for t, name, dtype, shape, dense in checks:
+        if (t.dtype is dtype and t.shape == shape and t.device == device
+                and (not dense or t.is_contiguous())):
+            continue
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+        if t.dtype is dtype and t.shape == shape:
+            raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name} must be {str(dtype).removeprefix('torch.')} {list(shape)}, got "
+                         f"{str(t.dtype).removeprefix('torch.')} {list(t.shape)}")
 
 
 def _rows(table, B, W):
@@ -102,7 +105,9 @@ def _call(device, stream, body):
     stream that the kernels run on current too, since that is where outputs and
     scratch space are allocated."""
     if stream is None and torch.cuda.current_device() == device.index:
-        return body(torch.cuda.current_stream(device).cuda_stream)
+        return body(_raw_stream(device.index))
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream must be on {device}, got {stream.device}")
     with _on(device):
         if stream is None:
             return body(torch.cuda.current_stream(device).cuda_stream)
@@ -113,7 +118,7 @@ def _call(device, stream, body):
 def _out(t, name, dtype, shape, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _want(t, name, dtype, shape)
+    _want(device, (t, name, dtype, shape, True))
     return t
 
 
@@ -125,16 +130,15 @@ def spec_verify_probs(target, draft, tokens, uniforms, draw_uniforms, *, out_acc
     Token x at position i is accepted when u q(x) < p(x); the first rejection's
     correction token is drawn from max(p - q, 0) by draw_uniforms, the bonus
     token from target row g.  Returns (accept_len [B], tokens [B, g+1])."""
-    dev = _same_device(target, draft, tokens, uniforms, draw_uniforms, out_accept_len, out_tokens)
-    dt = _dt(target)
+    dev, dt = _device(target), _dt(target)
     B, g1, V = _dims(target, "target", 3)
     g = g1 - 1
-    _want(target, "target", target.dtype, (B, g1, V))
+    _want(dev, (target, "target", target.dtype, (B, g1, V), True),
+          (tokens, "tokens", torch.int32, (B, g), True),
+          (uniforms, "uniforms", torch.float32, (B, g), True),
+          (draw_uniforms, "draw_uniforms", torch.float32, (B,), True))
     if draft is not None:
-        _want(draft, "draft", target.dtype, (B, g, V))
-    _want(tokens, "tokens", torch.int32, (B, g))
-    _want(uniforms, "uniforms", torch.float32, (B, g))
-    _want(draw_uniforms, "draw_uniforms", torch.float32, (B,))
+        _want(dev, (draft, "draft", target.dtype, (B, g, V), True))
 
     def body(s):
         acc = _out(out_accept_len, "out_accept_len", torch.int32, (B,), dev)
@@ -156,19 +160,17 @@ def spec_verify_tree(target, draft, tokens, parents, cu_nodes, uniforms, draw_un
     were drawn from (None for point drafts); tokens [N] int32, uniforms [N],
     draw_uniforms [B] fp32; max_nodes: the most nodes a sequence has.
     Returns (accept_len [B], tokens [B, max_nodes], path [B, max_nodes])."""
-    dev = _same_device(target, draft, tokens, parents, cu_nodes, uniforms, draw_uniforms,
-                       out_accept_len, out_tokens, out_path)
-    dt = _dt(target)
+    dev, dt = _device(target), _dt(target)
     N, V = _dims(target, "target", 2)
     B, = _dims(draw_uniforms, "draw_uniforms", 1)
-    _want(target, "target", target.dtype, (N, V))
+    _want(dev, (target, "target", target.dtype, (N, V), True),
+          (tokens, "tokens", torch.int32, (N,), True),
+          (parents, "parents", torch.int32, (N,), True),
+          (cu_nodes, "cu_nodes", torch.int32, (B + 1,), True),
+          (uniforms, "uniforms", torch.float32, (N,), True),
+          (draw_uniforms, "draw_uniforms", torch.float32, (B,), True))
     if draft is not None:
-        _want(draft, "draft", target.dtype, (N, V))
-    _want(tokens, "tokens", torch.int32, (N,))
-    _want(parents, "parents", torch.int32, (N,))
-    _want(uniforms, "uniforms", torch.float32, (N,))
-    _want(draw_uniforms, "draw_uniforms", torch.float32, (B,))
-    _want(cu_nodes, "cu_nodes", torch.int32, (B + 1,))
+        _want(dev, (draft, "draft", target.dtype, (N, V), True))
 
     def body(s):
         acc = _out(out_accept_len, "out_accept_len", torch.int32, (B,), dev)
@@ -194,21 +196,20 @@ def kv_slots(lens, add, cu_rows, block_table, free_pages, free_count, *, rows: i
     free_count [1]); slots is -1 for rows not kept, start -1 for a request that
     was refused (no pages, table row too short) or released.  out_lens and
     out_free_count may be lens and free_count."""
-    dev = _same_device(lens, add, cu_rows, block_table, free_pages, free_count, path, out_slots,
-                       out_start, out_lens, out_free_count)
+    dev = _device(lens)
     B, = _dims(lens, "lens", 1)
     W = _dims(block_table, "block_table", 2)[1]
     pool, = _dims(free_pages, "free_pages", 1)
-    width = 0 if path is None else _dims(path, "path", 2)[1]
-    _want(lens, "lens", torch.int32, (B,))
-    _want(add, "add", torch.int32, (B,))
-    _want(cu_rows, "cu_rows", torch.int32, (B + 1,))
-    _want(block_table, "block_table", torch.int32, (B, W), dense=False)
+    width = 0
+    _want(dev, (lens, "lens", torch.int32, (B,), True), (add, "add", torch.int32, (B,), True),
+          (cu_rows, "cu_rows", torch.int32, (B + 1,), True),
+          (block_table, "block_table", torch.int32, (B, W), False),
+          (free_pages, "free_pages", torch.int32, (pool,), True),
+          (free_count, "free_count", torch.int32, (1,), True))
     _rows(block_table, B, W)
-    _want(free_pages, "free_pages", torch.int32, (pool,))
-    _want(free_count, "free_count", torch.int32, (1,))
     if path is not None:
-        _want(path, "path", torch.int32, (B, width))
+        width = _dims(path, "path", 2)[1]
+        _want(dev, (path, "path", torch.int32, (B, width), True))
 
     def body(s):
         slots = _out(out_slots, "out_slots", torch.int32, (rows,), dev)
@@ -230,17 +231,16 @@ def kv_append(k, v, slots, k_cache, v_cache, *, stream=None):
     D]; slots (int32) outside the cache skip the row.  With a leading layer
     axis on all four, every layer at once.  Strides are free but for the last
     axis; k, v must not overlap the caches.  Returns None."""
-    dev = _same_device(k, v, slots, k_cache, v_cache)
+    dev, dt = _device(k), k.dtype
     shape = k.shape
     if len(shape) not in (3, 4):
         raise ValueError(f"k must be [N, H, D] or [layers, N, H, D], got {list(shape)}")
     lead = tuple(shape[:-3])
     N, H, D = shape[-3:]
     pages, page = _dims(k_cache, "k_cache", len(shape) + 1)[-4:-2]
-    _want(v, "v", k.dtype, shape, dense=False)
-    _want(k_cache, "k_cache", k.dtype, lead + (pages, page, H, D), dense=False)
-    _want(v_cache, "v_cache", k.dtype, lead + (pages, page, H, D), dense=False)
-    _want(slots, "slots", torch.int32, (N,))
+    cache = lead + (pages, page, H, D)
+    _want(dev, (v, "v", dt, shape, False), (k_cache, "k_cache", dt, cache, False),
+          (v_cache, "v_cache", dt, cache, False), (slots, "slots", torch.int32, (N,), True))
     es = k.element_size()
     if es not in (1, 2, 4):
         raise ValueError(f"elements of 1, 2 or 4 bytes are copied, got {k.dtype}")
@@ -276,8 +276,7 @@ def tree_attention(q, k, v, k_cache, v_cache, block_table, lens, parents, cu_nod
     defaults to D ** -0.5.  Returns (out [N, Hq, D], lse [N, Hq] fp32 or
     None).  `workspace`: a uint8 tensor of tree_attention_workspace_size
     bytes, of any content; calls that may run at once need one each."""
-    dev = _same_device(q, k, v, k_cache, v_cache, block_table, lens, parents, cu_nodes, out,
-                       out_lse, workspace)
+    dev = _device(q)
     dt = q.dtype
     if dt is not torch.bfloat16 and dt is not torch.float16:
         raise TypeError(f"q must be bfloat16 or float16, got {dt}")
@@ -286,14 +285,13 @@ def tree_attention(q, k, v, k_cache, v_cache, block_table, lens, parents, cu_nod
     pages, page = _dims(k_cache, "k_cache", 4)[:2]
     B, = _dims(lens, "lens", 1)
     W = _dims(block_table, "block_table", 2)[1]
-    _want(k, "k", dt, (N, Hkv, D), dense=False)
-    _want(v, "v", dt, (N, Hkv, D), dense=False)
-    _want(k_cache, "k_cache", dt, (pages, page, Hkv, D), dense=False)
-    _want(v_cache, "v_cache", dt, (pages, page, Hkv, D), dense=False)
-    _want(lens, "lens", torch.int32, (B,))
-    _want(cu_nodes, "cu_nodes", torch.int32, (B + 1,))
-    _want(parents, "parents", torch.int32, (N,))
-    _want(block_table, "block_table", torch.int32, (B, W), dense=False)
+    nodes, cache = (N, Hkv, D), (pages, page, Hkv, D)
+    _want(dev, (k, "k", dt, nodes, False), (v, "v", dt, nodes, False),
+          (k_cache, "k_cache", dt, cache, False), (v_cache, "v_cache", dt, cache, False),
+          (lens, "lens", torch.int32, (B,), True),
+          (cu_nodes, "cu_nodes", torch.int32, (B + 1,), True),
+          (parents, "parents", torch.int32, (N,), True),
+          (block_table, "block_table", torch.int32, (B, W), False))
     _rows(block_table, B, W)
     qs, ks, vs, kcs, vcs = q.stride(), k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
     if N > 0 and not qs[2] == ks[2] == vs[2] == kcs[3] == vcs[3] == 1:
@@ -305,7 +303,10 @@ def tree_attention(q, k, v, k_cache, v_cache, block_table, lens, parents, cu_nod
         if with_lse or lse is not None:
             lse = _out(lse, "out_lse", torch.float32, (N, Hq), dev)
         ws = workspace
-        if ws is None:
+        if ws is not None:
+            if ws.device != dev or not ws.is_contiguous():
+                raise ValueError(f"workspace must be contiguous on {dev}")
+        else:
             ws = torch.empty(max(tree_attention_workspace_size(Hq, Hkv, D), 256),
                              dtype=torch.uint8, device=dev)
         a = _AttentionArgs(

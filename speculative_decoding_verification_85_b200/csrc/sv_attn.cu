@@ -39,6 +39,7 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 128;          // keys of a tile, rows of a query tile
+constexpr int kHalf = 64;           // keys of a step
 constexpr int kWarpsSoft = 8;       // softmax warps: two groups of four
 constexpr int kWarpV = 9, kWarpMma = 10;  // 8: keys, 9: values, 10 and 11: products of each softmax group
 constexpr int kThreads = 32 * 12;
@@ -149,7 +150,8 @@ constexpr int kParts = 8;
 
 struct Shared {
   uint64_t full[8], empty[8];
-  uint64_t qfull[2], sfull[2], pready[2], pvdone[2], oempty[2], turn[2], drain[2], meet, met;
+  uint64_t sfull[2][2], pready[2][2], pvdone[2][2];  // [group][step & 1]
+  uint64_t qfull[2], oempty[2], drain[2], meet, met;
   float2 xch[2][kTile];       // [group][row]: shift, sum
   int64_t scan[16];
   Walk start;                 // the stretch (left == 0: nothing for this CTA)
@@ -247,11 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.qfull[i], 1);
-      mbar_init(&sh.sfull[i], 1);
-      mbar_init(&sh.pready[i], kTile);
-      mbar_init(&sh.pvdone[i], 1);
+      for (int e = 0; e < 2; ++e) {
+        mbar_init(&sh.sfull[i][e], 1);
+        mbar_init(&sh.pready[i][e], kTile);
+        mbar_init(&sh.pvdone[i][e], 1);
+      }
       mbar_init(&sh.oempty[i], kWarpsSoft);
-      mbar_init(&sh.turn[i], kWarpsSoft / 2);
       mbar_init(&sh.drain[i], 1);
     }
     mbar_init(&sh.meet, 2);
@@ -337,6 +340,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   asm volatile("griddepcontrol.launch_dependents;");
   const uint32_t tmem = sh.tmem;
   // Part `seg`; every reader takes them all, in order, and gives each back (freed).
+  // Keys of tile j of a unit; a tile of more than kHalf takes two steps.
+  auto keys_of = [&](const Part& w, int j) {
+    return min(kTile, j < w.tt ? min(w.n, SV_MAX_NODES) - (w.tt - 1 - j) * kTile : w.len - (j - w.tt) * kTile);
+  };
   auto part_of = [&](int seg, Part& w) {
     const bool ok = wait(sh, &sh.parted[seg % kParts], (seg / kParts) & 1);
     if (!__all_sync(0xffffffffu, ok)) return false;
@@ -445,19 +452,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       // warp keeps the books, one lane issues
       const int s = warp - kWarpMma;
       const bool issuer = elect_one();
-      constexpr uint32_t idesc_s = instr_desc(kBf16, kTile, false);
+      constexpr uint32_t idesc_s = instr_desc(kBf16, kHalf, false);
       constexpr uint32_t idesc_o = instr_desc(kBf16, DP, true);
-      constexpr int kStep = S::kTileBytes >> 4;  // from one tile's descriptor to the next's
+      constexpr int kStep = S::kTileBytes >> 4;       // from one tile's descriptor to the next's
+      constexpr int kHalfStep = (kHalf * 128) >> 4;   // from a tile's first keys to its second ones
       const int ksteps = cdiv(P.D, 16);
       const uint64_t qdesc = smem_desc(smem_addr(qtile) + s * S::kTileBytes, 16);
       const uint64_t kdesc = smem_desc(smem_addr(ring), 16);
       const uint64_t vdesc = smem_desc(smem_addr(ring), kTile * 128);
       const uint32_t s_at = tmem + s * kTile, o_at = tmem + 2 * kTile + s * kTile;
       int t0 = 0;  // tiles so far
-      // second products, query tiles loaded, parts with steps, parts with two query tiles so far
-      uint32_t npv = 0, nq = 0, nown = 0, ntwo = 0;
-      // steps of this group in the part that begins at tile t
-      auto steps_of = [&](const Part& x, int t) {
+      // query tiles loaded, parts with steps, parts with two query tiles so far; first and second
+      // products so far (step k uses S buffer k % 2)
+      uint32_t nq = 0, nown = 0, ntwo = 0, ns = 0, npv = 0;
+      // this group's tiles in the part that begins at tile t
+      auto tiles_of = [&](const Part& x, int t) {
         const int T = x.j1 - x.j0;
         return x.two ? T : (T + 1 - ((s ^ t) & 1)) / 2;
       };
@@ -482,28 +491,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         return got;
       };
       bool more = next_part();
-      if (more && steps_of(w, 0)) load_q(w);
+      if (more && tiles_of(w, 0)) load_q(w);
       while (ok && more) {
         const bool two = w.two;
-        const int steps = steps_of(w, t0), stride = two ? 1 : 2;
-        int t = two ? t0 : t0 + ((s ^ t0) & 1);  // own tile
+        const int tiles = tiles_of(w, t0), stride = two ? 1 : 2;
+        const int first = two ? t0 : t0 + ((s ^ t0) & 1);  // own first tile
+        const int base = w.j0 - t0;                          // from a tile of the CTA to the unit's
         t0 += w.j1 - w.j0;
-        auto scores = [&]() {  // S of tile t
-          const int st = S::stage(t);
-          if (!__all_sync(0xffffffffu, wait(sh, &sh.full[st], S::parity(t)))) return false;
+        // the next first and second product: tile, its half, whether a half is left
+        int ta = first, ha = 0, ka = tiles, tb = first, hb = 0, kb = tiles;
+        auto scores = [&]() {  // S of the next keys, once the weights of two steps ago are used
+          const int st = S::stage(ta), buf = ns & 1;
+          bool fine = ns < 2 || wait(sh, &sh.pvdone[s][buf], ((ns >> 1) - 1) & 1);
+          fine = fine && wait(sh, &sh.full[st], S::parity(ta));
+          if (!__all_sync(0xffffffffu, fine)) return false;
+          const bool last = ha == 1 || keys_of(w, base + ta) <= kHalf;
           tc_fence_after();
           if (issuer) {
-            const uint64_t db = kdesc + st * kStep;
+            const uint64_t db = kdesc + st * kStep + ha * kHalfStep;
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) {
               const int off = ((i >> 2) * (kTile * 128) + (i & 3) * 32) >> 4;
-              if (i < ksteps) mma_ss(s_at, qdesc + off, db + off, idesc_s, i > 0);
+              if (i < ksteps) mma_ss(s_at + buf * kHalf, qdesc + off, db + off, idesc_s, i > 0);
             }
-            mma_commit(&sh.sfull[s]);
-            mma_commit(&sh.empty[st]);
-            if (!two) mma_commit(&sh.empty[st]);  // (the other group's share)
+            mma_commit(&sh.sfull[s][buf]);
+            if (last) {
+              mma_commit(&sh.empty[st]);
+              if (!two) mma_commit(&sh.empty[st]);  // (the other group's share)
+            }
           }
           __syncwarp();
+          ++ns;
+          ha ^= 1;
+          if (last) {
+            ha = 0;
+            ta += stride;
+            --ka;
+          }
           return true;
         };
         if (two) {  // the other group has passed all tiles before this part, too
@@ -512,35 +536,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           if (!ok) break;
           ++ntwo;
         }
-        if (steps > 0) {
-          ok = (npv == 0 || wait(sh, &sh.pvdone[s], (npv - 1) & 1)) && wait(sh, &sh.qfull[s], (nq - 1) & 1);
-          ok = __all_sync(0xffffffffu, ok) && scores();
+        if (tiles > 0) {
+          ok = __all_sync(0xffffffffu, wait(sh, &sh.qfull[s], (nq - 1) & 1));
+          ok = ok && scores() && (ka == 0 || scores());
           if (ok && nown > 0) ok = __all_sync(0xffffffffu, wait(sh, &sh.oempty[s], (nown - 1) & 1));
           ++nown;
         }
-        for (int i = 0; ok && i < steps; ++i) {
-          const int st = S::stage(t) + 1;
-          ok = wait(sh, &sh.full[st], S::parity(t)) && wait(sh, &sh.pready[s], npv & 1);
+        for (bool fresh = true; ok && kb > 0; fresh = false) {
+          const int st = S::stage(tb) + 1, buf = npv & 1;
+          ok = wait(sh, &sh.full[st], S::parity(tb)) && wait(sh, &sh.pready[s][buf], (npv >> 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          const bool last = hb == 1 || keys_of(w, base + tb) <= kHalf;
           tc_fence_after();
           if (issuer) {
-            const uint64_t db = vdesc + st * kStep;
+            const uint64_t db = vdesc + st * kStep + hb * kHalfStep;
 #pragma unroll
-            for (int q = 0; q < kTile / 16; ++q) mma_ts(o_at, s_at + q * 8, db + q * (2048 >> 4), idesc_o, q > 0 || i > 0);
-            mma_commit(&sh.pvdone[s]);
-            mma_commit(&sh.empty[st]);
-            if (!two) mma_commit(&sh.empty[st]);
+            for (int q = 0; q < kHalf / 16; ++q)
+              mma_ts(o_at, s_at + buf * kHalf + q * 8, db + q * (2048 >> 4), idesc_o, q > 0 || !fresh);
+            mma_commit(&sh.pvdone[s][buf]);
+            if (last) {
+              mma_commit(&sh.empty[st]);
+              if (!two) mma_commit(&sh.empty[st]);
+            }
           }
           __syncwarp();
-          t += stride;
           ++npv;
-          // the next S takes the place of the weights just used
-          if (i + 1 < steps) ok = __all_sync(0xffffffffu, wait(sh, &sh.pvdone[s], (npv - 1) & 1)) && scores();
+          hb ^= 1;
+          if (last) {
+            hb = 0;
+            tb += stride;
+            --kb;
+          }
+          // (the softmax of the step in between is under way meanwhile)
+          if (ka > 0) ok = scores();
         }
         // the part's last S is done: its query tile can go
         more = ok && next_part();
-        if (more && steps_of(w, t0)) load_q(w);
+        if (more && tiles_of(w, t0)) load_q(w);
       }
       if (!ok) {  // let the products and the copy in flight end
         if (issuer) mma_commit(&sh.drain[s]);
@@ -561,26 +594,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const uint32_t s_at = tmem + lanes + wg * kTile, o_at = tmem + lanes + 2 * kTile;
     const float sl = P.sl;
     int t0 = 0, dseg = 0;       // tiles and parts so far
-    uint32_t steps_done = 0;    // steps of this group so far
-    uint32_t turns = 0;         // turns of this group so far
+    uint32_t step = 0;          // steps of this group so far
     bool alive = true;
     float shift = 0.0f, sum = 0.0f;  // this row's exponent shift (base 2) and sum of weights
 
-    // S of one key tile to P: shift, sum and, when a maximum has grown much, the accumulator.
-    // With two query tiles the groups take turns at the exponentials, so that one's run beside
-    // the other's products: group 0's turn k + 1 follows group 1's turn k.  False: a wait failed.
-    auto weigh = [&](bool fresh, bool mine, bool two) {
-      float x[kTile];
+    // S of one step's keys to P: shift, sum and, when a maximum has grown much, the accumulator
+    // (once the second product of the step before is done).  False: a wait failed.
+    auto weigh = [&](bool fresh, bool mine) {
+      const uint32_t at = s_at + (step & 1) * kHalf;
+      float x[kHalf];
 #pragma unroll
-      for (int c = 0; c < kTile; c += 32) tmem_ld32(s_at + c, x + c);
+      for (int c = 0; c < kHalf; c += 32) tmem_ld32(at + c, x + c);
       tc_wait_ld();
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < kTile; c += 2) mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], x[c]), x[c + 1]);
+      for (int c = 0; c < kHalf; c += 2) mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], x[c]), x[c + 1]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
       if (fresh) {
         shift = top;
       } else if (__any_sync(0xffffffffu, mine && top - shift > kGrow)) {
+        if (!__all_sync(0xffffffffu, wait(sh, &sh.pvdone[wg][(step - 1) & 1], ((step - 1) >> 1) & 1))) return false;
+        tc_fence_after();
         const float now = fmaxf(shift, top);
         const float f = now == shift ? 1.0f : ex2_approx(shift - now);
         shift = now;
@@ -595,13 +629,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           tmem_st16(o_at + wg * kTile + c, reinterpret_cast<uint32_t*>(o));
         }
       }
-      if (two && (wg || turns > 0) && !__all_sync(0xffffffffu, wait(sh, &sh.turn[wg], (turns - (wg ? 0 : 1)) & 1)))
-        return false;
       const float neg = shift == -INFINITY ? 0.0f : -shift;
       const uint64_t sl2 = pair(sl, sl), neg2 = pair(neg, neg);
       uint64_t part[2] = {0, 0};
 #pragma unroll
-      for (int c0 = 0; c0 < kTile; c0 += 32) {
+      for (int c0 = 0; c0 < kHalf; c0 += 32) {
         // weights rounded to the input type (relative 2^-8 / 2^-11 at most, as the output
         // itself is, and averaged over the keys); the sum takes them unrounded
         uint32_t pk[16];
@@ -612,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           part[(c >> 1) & 1] = add2(part[(c >> 1) & 1], pair(a, b));
           pk[c >> 1] = pack2<kBf16>(a, b);
         }
-        tmem_st16(s_at + (c0 >> 1), pk);
+        tmem_st16(at + (c0 >> 1), pk);
       }
       const uint64_t p = add2(part[0], part[1]);
       sum += pair_lo(p) + pair_hi(p);
@@ -634,14 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       shift = -INFINITY;
       sum = 0.0f;
       int up = mine ? node : -1;  // next ancestor to pass
-      // the groups' steps in this part (with one query tile tile t is group t % 2's)
-      const int steps0 = w.two ? T : (T + 1 - (t0 & 1)) / 2, steps1 = w.two ? T : T - steps0;
-      const int mysteps = wg ? steps1 : steps0;
-      for (int i = 0; i < mysteps; ++i) {
+      // the groups' tiles in this part (with one query tile tile t is group t % 2's)
+      const int tiles0 = w.two ? T : (T + 1 - (t0 & 1)) / 2, tiles1 = w.two ? T : T - tiles0;
+      const int mytiles = wg ? tiles1 : tiles0;
+      for (int i = 0; alive && i < mytiles; ++i) {
         const int tile = w.two ? i : 2 * i + ((wg ^ t0) & 1), j = w.j0 + tile;
         const bool tree = j < w.tt;
         const int first = (tree ? w.tt - 1 - j : j - w.tt) * kTile;
-        const int valid = (tree ? min(w.n, SV_MAX_NODES) : w.len) - first;
+        const int valid = keys_of(w, j);
         const bool special = tree || valid < kTile;
         uint32_t see[4];
         if (special) {
@@ -668,46 +700,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
           }
         }
-        alive = __all_sync(0xffffffffu, wait(sh, &sh.sfull[wg], steps_done & 1));
-        if (!alive) break;
-        ++steps_done;
-        if (busy) {
-          tc_fence_after();
-          if (special) {  // -inf for the keys that do not count
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t m = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
-              float x[32];
-              tmem_ld32(s_at + 32 * q, x);
-              tc_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(m >> c & 1)) x[c] = -INFINITY;
-              tmem_st32(s_at + 32 * q, reinterpret_cast<uint32_t*>(x));
-            }
-            tc_wait_st();
-          }
-          alive = weigh(i == 0, mine, w.two);
-          tc_fence_before();
-        } else if (w.two && (wg || turns > 0)) {
-          alive = __all_sync(0xffffffffu, wait(sh, &sh.turn[wg], (turns - (wg ? 0 : 1)) & 1));
-        }
-        if (!alive) break;
-        if (w.two) {
-          ++turns;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.turn[wg ^ 1]);
-        }
-        if (special) {
-          // Rows of the value tile that hold no key of this tile weigh nothing, but a weight of
-          // zero does not silence what they may hold: they are cleared, and so are infinities
-          // and NaN in the nodes' own values (added back at the end to the rows that see them).
-          // With two query tiles both groups do it, to the same effect.  (Only now: S of this tile
-          // says that the value stage's last lap is over.)
-          const int st = S::stage(t0 + tile) + 1;
-          alive = __all_sync(0xffffffffu, wait(sh, &sh.full[st], S::parity(t0 + tile)));
+        for (int half = 0; half * kHalf < valid; ++half) {
+          alive = __all_sync(0xffffffffu, wait(sh, &sh.sfull[wg][step & 1], (step >> 1) & 1));
           if (!alive) break;
-          {
+          if (busy) {
+            tc_fence_after();
+            if (special) {  // -inf for the keys that do not count
+              const uint32_t at = s_at + (step & 1) * kHalf;
+#pragma unroll 1
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t m = half ? (q ? see[3] : see[2]) : (q ? see[1] : see[0]);
+                float x[32];
+                tmem_ld32(at + 32 * q, x);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(m >> c & 1)) x[c] = -INFINITY;
+                tmem_st32(at + 32 * q, reinterpret_cast<uint32_t*>(x));
+              }
+              tc_wait_st();
+            }
+            alive = weigh(i == 0 && half == 0, mine);
+            if (!alive) break;
+            tc_fence_before();
+          }
+          if (special && half == 0) {
+            // Rows of the value tile that hold no key of this tile weigh nothing, but a weight of
+            // zero does not silence what they may hold: they are cleared, and so are infinities
+            // and NaN in the nodes' own values (added back at the end to the rows that see them).
+            // With two query tiles both groups do it, to the same effect.  (S of this tile says
+            // that the second product two steps ago is done, and a tile of one step only is
+            // special itself: the last lap of the value stage has been seen to be over.)
+            const int st = S::stage(t0 + tile) + 1;
+            alive = __all_sync(0xffffffffu, wait(sh, &sh.full[st], S::parity(t0 + tile)));
+            if (!alive) break;
             char* vt = ring + st * S::kTileBytes + r * 128;
             if (r >= valid) {
 #pragma unroll
@@ -730,16 +757,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
+          mbar_arrive(&sh.pready[wg][step & 1]);
+          ++step;
         }
-        mbar_arrive(&sh.pready[wg]);
       }
+      if (!alive) break;
       // ---- the part's result
-      if (alive && mysteps > 0) alive = __all_sync(0xffffffffu, wait(sh, &sh.pvdone[wg], (steps_done - 1) & 1));
+      if (mytiles > 0) alive = __all_sync(0xffffffffu, wait(sh, &sh.pvdone[wg][(step - 1) & 1], ((step - 1) >> 1) & 1));
       if (!alive) break;
       if (bad) sum = NAN;
       // (A group writes here again behind second products that wait for all warps to have left
       // its last part with steps; badv of two parts ahead was last read two meetings ago.)
-      if (mysteps > 0) sh.xch[wg][r] = make_float2(shift, sum);
+      if (mytiles > 0) sh.xch[wg][r] = make_float2(shift, sum);
       if (tid == 0) sh.badv[(buf + 2) & 3] = 0;
       tc_fence_before();
       __syncwarp();
@@ -751,8 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const bool join = !w.two;  // both groups hold parts of the same rows
       float f0 = 1.0f, f1 = 0.0f;
       if (join) {
-        const float2 a = steps0 > 0 ? sh.xch[0][r] : make_float2(-INFINITY, 0.0f);
-        const float2 b = steps1 > 0 ? sh.xch[1][r] : make_float2(-INFINITY, 0.0f);
+        const float2 a = tiles0 > 0 ? sh.xch[0][r] : make_float2(-INFINITY, 0.0f);
+        const float2 b = tiles1 > 0 ? sh.xch[1][r] : make_float2(-INFINITY, 0.0f);
         const float now = fmaxf(a.x, b.x);
         f0 = a.x == -INFINITY ? 0.0f : ex2_approx(a.x - now);
         f1 = b.x == -INFINITY ? 0.0f : ex2_approx(b.x - now);
@@ -772,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         for (int c = cbeg; c < cend; c += 16) {
           // with steps of one group alone, its accumulator is the result
           float o[16];
-          tmem_ld16(o_at + (join ? steps0 == 0 : wg) * kTile + c, o);
+          tmem_ld16(o_at + (join ? tiles0 == 0 : wg) * kTile + c, o);
           if (join && T > 1) {
             float o1[16];
             tmem_ld16(o_at + kTile + c, o1);
@@ -815,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (steps0 > 0) mbar_arrive(&sh.oempty[0]);
-        if (steps1 > 0) mbar_arrive(&sh.oempty[1]);
+        if (tiles0 > 0) mbar_arrive(&sh.oempty[0]);
+        if (tiles1 > 0) mbar_arrive(&sh.oempty[1]);
       }
       if (mine && (!join || wg == 0)) {
         if (whole) {
