@@ -7,6 +7,12 @@ It performs no computation of its own and has no CPU fallback: importing it
 without the built library, or calling it on tensors that are not on a CUDA
 device, raises.  The same library holds the host-side draft selector
 (``include/sv_bandit.h``, native C++), bound here as ``Bandit``.
+
+Around the verification of drafted trees (``include/spec_tree.h``):
+``tree_attention`` over a paged cache, ``spec_verify_probs`` /
+``spec_verify_tree`` from given probabilities and random numbers, ``kv_slots``
+and ``kv_append``, and ``PagedCache``, which keeps the cache and its
+bookkeeping on the device.
 """
 from ._binding import (  # noqa: F401
     BF16, F32, SHARD_ALIGN, Bandit, SpecVerifyError, Verifier, gather_records, lib, library_path,
@@ -16,6 +22,7 @@ from ._binding import (  # noqa: F401
     spec_verify_shard_stats, spec_verify_vocab_sharded, staging_size, vocab_shards,
     workspace_size,
 )
+from .cache import PagedCache  # noqa: F401
 from ._tree import (  # noqa: F401
     MAX_NODES, kv_append, kv_slots, spec_verify_probs, spec_verify_tree, tree_attention,
     tree_attention_workspace_size,
@@ -28,6 +35,6 @@ __all__ = [
     "spec_verify_shard_stats", "spec_verify_shard_decide", "spec_verify_shard_pick",
     "spec_verify_vocab_sharded", "vocab_shards", "shard_stats_bytes", "shard_candidate_bytes",
     "gather_records", "SHARD_ALIGN",
-    "spec_verify_probs", "spec_verify_tree", "kv_slots", "kv_append", "MAX_NODES",
+    "spec_verify_probs", "spec_verify_tree", "kv_slots", "kv_append", "MAX_NODES", "PagedCache",
     "tree_attention", "tree_attention_workspace_size",
 ]

@@ -63,7 +63,7 @@ int check_device() {
   return SV_OK;
 }
 
-int allow_kernel(const void* kernel, size_t smem, bool large_clusters) {
+int allow_smem(const void* kernel, size_t smem) {
   static std::mutex mu;
   static std::set<std::pair<int, const void*>> done;
   int dev = 0;
@@ -72,8 +72,6 @@ int allow_kernel(const void* kernel, size_t smem, bool large_clusters) {
   std::lock_guard<std::mutex> lk(mu);
   if (done.count({dev, kernel})) return SV_OK;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e == cudaSuccess && large_clusters)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   done.insert({dev, kernel});
   return SV_OK;

@@ -1102,7 +1102,7 @@ template <int DP, bool kBf16>
 int launch_attn(const AttnParams& p, int ctas, cudaStream_t stream) {
   constexpr size_t kSmem = Shape<DP>::kTiles + sizeof(Shared);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
-  int rc = allow_kernel(reinterpret_cast<const void*>(attn_kernel<DP, kBf16>), kSmem, false);
+  int rc = allow_smem(reinterpret_cast<const void*>(attn_kernel<DP, kBf16>), kSmem);
   if (rc != SV_OK) return rc;
   attn_kernel<DP, kBf16><<<ctas, kThreads, kSmem, stream>>>(p);
   if ((rc = check_launch("tree attention")) != SV_OK) return rc;

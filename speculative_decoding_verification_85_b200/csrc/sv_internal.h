@@ -90,9 +90,8 @@ size_t multidraft_global_bytes(int B, int V);  // residual laws of the multi-dra
 int set_error(int status, const char* fmt, ...);
 int check_device();
 int check_launch(const char* what);
-// Once per kernel and device: allow `smem` bytes of dynamic shared memory and,
-// where asked, clusters of more than eight blocks.
-int allow_kernel(const void* kernel, size_t smem, bool large_clusters);
+// Once per kernel and device: allow `smem` bytes of dynamic shared memory.
+int allow_smem(const void* kernel, size_t smem);
 
 // Kernel launchers (sv_single.cu / sv_multi.cu).
 int launch_single(const void* target, const void* draft, const int32_t* tokens,

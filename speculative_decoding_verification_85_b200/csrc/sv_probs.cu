@@ -26,7 +26,7 @@ namespace {
 constexpr int kPThreads = 256;
 constexpr int kPWarps = kPThreads / 32;
 constexpr int kChunk = 512;  // entries one warp sums at a time
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 constexpr size_t kMaxSmem = 200 * 1024;
 
 struct ProbsParams {
@@ -448,16 +448,19 @@ __global__ void __launch_bounds__(kPThreads) probs_kernel(const __grid_constant_
 template <bool kBf16>
 int launch_probs(ProbsParams p, int B, cudaStream_t stream) {
   const int nch = static_cast<int>((static_cast<int64_t>(p.V) + kChunk - 1) / kChunk);
-  // Cluster size: enough CTAs for four a SM, no slice below one chunk a warp.
+  // Cluster size: one CTA a sequence where the sequences fill the SMs, else enough for four a
+  // SM, with no slice below one chunk a warp.  (256 sequences of V = 151936 fp32: 61 us with
+  // one CTA each, 64 with four; 64 trees of V = 128256 bf16: 56 us with four, 44 with eight.)
   int C = 1;
-  while (C < kMaxCluster && B * C < 4 * 148 && nch > C * kPWarps) C *= 2;
+  if (B < 148)
+    while (C < kMaxCluster && B * C < 4 * 148 && nch > C * kPWarps) C *= 2;
   p.cluster = C;
   p.chunks = (nch + C - 1) / C;
   const int cap = p.tree ? (p.width < SV_MAX_NODES ? p.width : SV_MAX_NODES) : p.gamma + 1;
   const size_t smem = static_cast<size_t>(p.chunks) * sizeof(double) + static_cast<size_t>(cap) * 7 * 4;
   if (smem > kMaxSmem)
     return set_error(SV_ERR_UNSUPPORTED, "V = %d is too large for B = %d", p.V, B);
-  const int rc = allow_kernel(reinterpret_cast<const void*>(probs_kernel<kBf16>), kMaxSmem, true);
+  const int rc = allow_smem(reinterpret_cast<const void*>(probs_kernel<kBf16>), kMaxSmem);
   if (rc != SV_OK) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(B) * C);
