@@ -41,12 +41,14 @@ namespace {
 constexpr int kTile = 128;          // keys of a tile, rows of a query tile
 constexpr int kHalf = 64;           // keys of a step
 constexpr int kWarpsSoft = 8;       // softmax warps: two groups of four
-constexpr int kWarpV = 9, kWarpMma = 10;  // 8: keys, 9: values, 10 and 11: products of each softmax group
-constexpr int kThreads = 32 * 12;
-// Registers: the two softmax groups hold a row of 128 scores a thread, the
-// third group needs few.  2 x 208 + 88 = 3 x 168, what a block of 384 threads
-// is launched with.
-constexpr int kRegsSoft = 208, kRegsRest = 88;
+// Warps 0-7: softmax; 8: keys, 9: values; 10 and 11: first products of each
+// softmax group; 12 and 13: second products (apart, since each would wait for
+// the other's turn).
+constexpr int kWarpV = 9, kWarpS = 10, kWarpO = 12;
+constexpr int kThreads = 32 * 16;     // (the last two warps only fill their warpgroup)
+// Registers: the softmax groups hold 64 scores a thread, the others need few.
+// 2 x 168 + 2 x 88 = 4 x 128, what a block of 512 threads is launched with.
+constexpr int kRegsSoft = 168, kRegsRest = 88;
 constexpr float kGrow = 8.0f;       // base-2 growth of a maximum that is let stand
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxCtas = 160;         // SMs of a device, with room
@@ -151,7 +153,7 @@ constexpr int kParts = 8;
 struct Shared {
   uint64_t full[8], empty[8];
   uint64_t sfull[2][2], pready[2][2], pvdone[2][2];  // [group][step & 1]
-  uint64_t qfull[2], oempty[2], drain[2], meet, met;
+  uint64_t qfull[2], oempty[2], drain[4], meet[2], met;
   float2 xch[2][kTile];       // [group][row]: shift, sum
   int64_t scan[16];
   Walk start;                 // the stretch (left == 0: nothing for this CTA)
@@ -255,13 +257,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         mbar_init(&sh.pvdone[i][e], 1);
       }
       mbar_init(&sh.oempty[i], kWarpsSoft);
-      mbar_init(&sh.drain[i], 1);
+      mbar_init(&sh.meet[i], 2);
     }
-    mbar_init(&sh.meet, 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.drain[i], 1);
     mbar_init(&sh.met, kWarpsSoft);
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&sh.parted[i], 1);
-      mbar_init(&sh.freed[i], kWarpsSoft + 3);  // softmax, values and products
+      mbar_init(&sh.freed[i], kWarpsSoft + 5);  // softmax, values and products
     }
     for (int i = 0; i < 4; ++i) sh.badv[i] = 0;
     mbar_init_fence();
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const CUtensorMap* maps = &P.qmap;
     asm volatile("prefetch.tensormap [%0];" ::"l"(maps + (tid - 32)) : "memory");
   }
-  if (warp == kWarpMma) {
+  if (warp == kWarpS) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
   if (warp >= kWarpsSoft) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp < kWarpMma) {
+    if (warp < kWarpS) {
       // -------------------------------------------------- keys and values
       // one warp each
       const bool kv = warp == kWarpV;
@@ -446,43 +448,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         }
       }
       __syncwarp();
-    } else {
+    } else if (warp < kWarpO + 2) {
       // --------------------------------------------------------- products
-      // one warp for each softmax group, with the group's own copy of its query tile; the whole
-      // warp keeps the books, one lane issues
-      const int s = warp - kWarpMma;
+      // a warp for each kind and softmax group; the whole warp keeps the books, one lane issues
+      const int s = (warp - kWarpS) & 1;
       const bool issuer = elect_one();
-      constexpr uint32_t idesc_s = instr_desc(kBf16, kHalf, false);
-      constexpr uint32_t idesc_o = instr_desc(kBf16, DP, true);
       constexpr int kStep = S::kTileBytes >> 4;       // from one tile's descriptor to the next's
       constexpr int kHalfStep = (kHalf * 128) >> 4;   // from a tile's first keys to its second ones
-      const int ksteps = cdiv(P.D, 16);
-      const uint64_t qdesc = smem_desc(smem_addr(qtile) + s * S::kTileBytes, 16);
-      const uint64_t kdesc = smem_desc(smem_addr(ring), 16);
-      const uint64_t vdesc = smem_desc(smem_addr(ring), kTile * 128);
       const uint32_t s_at = tmem + s * kTile, o_at = tmem + 2 * kTile + s * kTile;
-      int t0 = 0;  // tiles so far
-      // query tiles loaded, parts with steps, parts with two query tiles so far; first and second
-      // products so far (step k uses S buffer k % 2)
-      uint32_t nq = 0, nown = 0, ntwo = 0, ns = 0, npv = 0;
-      // this group's tiles in the part that begins at tile t
-      auto tiles_of = [&](const Part& x, int t) {
-        const int T = x.j1 - x.j0;
-        return x.two ? T : (T + 1 - ((s ^ t) & 1)) / 2;
-      };
-      auto load_q = [&](const Part& x) {
-        if (issuer) {
-          mbar_arrive_expect_tx(&sh.qfull[s], P.npt * P.G * 128 * S::kHalves);
-#pragma unroll
-          for (int hf = 0; hf < S::kHalves; ++hf)
-            tma_3d(qtile + s * S::kTileBytes + hf * (kTile * 128), &P.qmap, hf * 64, x.h * P.G,
-                   x.lo + (x.u * 2 + (x.two ? s : 0)) * P.npt, &sh.qfull[s]);
-        }
-        __syncwarp();
-        ++nq;
-      };
+      int t0 = 0, seg = 0;              // tiles and parts so far
+      uint32_t n = 0, ntwo = 0;         // products, parts with two query tiles so far
       bool ok = true;
-      int seg = 0;
       Part w;
       auto next_part = [&]() {
         const bool got = part_of(seg, w);
@@ -490,97 +466,119 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         ++seg;
         return got;
       };
+      // this group's tiles in the part that begins at tile t
+      auto tiles_of = [&]() {
+        const int T = w.j1 - w.j0;
+        return w.two ? T : (T + 1 - ((s ^ t0) & 1)) / 2;
+      };
+      // before a part with two query tiles: the other group has passed all tiles up to here, too
+      auto meet = [&](uint64_t* bar) {
+        if (issuer) mbar_arrive(bar);
+        return __all_sync(0xffffffffu, wait(sh, bar, ntwo++ & 1));
+      };
       bool more = next_part();
-      if (more && tiles_of(w, 0)) load_q(w);
-      while (ok && more) {
-        const bool two = w.two;
-        const int tiles = tiles_of(w, t0), stride = two ? 1 : 2;
-        const int first = two ? t0 : t0 + ((s ^ t0) & 1);  // own first tile
-        const int base = w.j0 - t0;                          // from a tile of the CTA to the unit's
-        t0 += w.j1 - w.j0;
-        // the next first and second product: tile, its half, whether a half is left
-        int ta = first, ha = 0, ka = tiles, tb = first, hb = 0, kb = tiles;
-        auto scores = [&]() {  // S of the next keys, once the weights of two steps ago are used
-          const int st = S::stage(ta), buf = ns & 1;
-          bool fine = ns < 2 || wait(sh, &sh.pvdone[s][buf], ((ns >> 1) - 1) & 1);
-          fine = fine && wait(sh, &sh.full[st], S::parity(ta));
-          if (!__all_sync(0xffffffffu, fine)) return false;
-          const bool last = ha == 1 || keys_of(w, base + ta) <= kHalf;
-          tc_fence_after();
-          if (issuer) {
-            const uint64_t db = kdesc + st * kStep + ha * kHalfStep;
+      if (warp < kWarpO) {
+        // S of a step's keys, step n into buffer n % 2 once its weights of two steps ago are used
+        constexpr uint32_t idesc = instr_desc(kBf16, kHalf, false);
+        const int ksteps = cdiv(P.D, 16);
+        const uint64_t qdesc = smem_desc(smem_addr(qtile) + s * S::kTileBytes, 16);
+        const uint64_t kdesc = smem_desc(smem_addr(ring), 16);
+        uint32_t nq = 0;  // query tiles so far: the group's own copy
+        while (ok && more) {
+          const bool two = w.two;
+          const int tiles = tiles_of(), stride = two ? 1 : 2;
+          int t = two ? t0 : t0 + ((s ^ t0) & 1), j = w.j0 + t - t0;
+          if (tiles > 0) {
+            // the query tile's place is free once the last S from it is complete
+            if (n > 0) ok = __all_sync(0xffffffffu, wait(sh, &sh.sfull[s][(n - 1) & 1], ((n - 1) >> 1) & 1));
+            if (!ok) break;
+            if (issuer) {
+              mbar_arrive_expect_tx(&sh.qfull[s], P.npt * P.G * 128 * S::kHalves);
 #pragma unroll
-            for (int i = 0; i < DP / 16; ++i) {
-              const int off = ((i >> 2) * (kTile * 128) + (i & 3) * 32) >> 4;
-              if (i < ksteps) mma_ss(s_at + buf * kHalf, qdesc + off, db + off, idesc_s, i > 0);
+              for (int hf = 0; hf < S::kHalves; ++hf)
+                tma_3d(qtile + s * S::kTileBytes + hf * (kTile * 128), &P.qmap, hf * 64, w.h * P.G,
+                       w.lo + (w.u * 2 + (two ? s : 0)) * P.npt, &sh.qfull[s]);
             }
-            mma_commit(&sh.sfull[s][buf]);
-            if (last) {
-              mma_commit(&sh.empty[st]);
-              if (!two) mma_commit(&sh.empty[st]);  // (the other group's share)
-            }
+            __syncwarp();
+            ++nq;
           }
-          __syncwarp();
-          ++ns;
-          ha ^= 1;
-          if (last) {
-            ha = 0;
-            ta += stride;
-            --ka;
-          }
-          return true;
-        };
-        if (two) {  // the other group has passed all tiles before this part, too
-          if (issuer) mbar_arrive(&sh.meet);
-          ok = __all_sync(0xffffffffu, wait(sh, &sh.meet, ntwo & 1));
-          if (!ok) break;
-          ++ntwo;
-        }
-        if (tiles > 0) {
-          ok = __all_sync(0xffffffffu, wait(sh, &sh.qfull[s], (nq - 1) & 1));
-          ok = ok && scores() && (ka == 0 || scores());
-          if (ok && nown > 0) ok = __all_sync(0xffffffffu, wait(sh, &sh.oempty[s], (nown - 1) & 1));
-          ++nown;
-        }
-        for (bool fresh = true; ok && kb > 0; fresh = false) {
-          const int st = S::stage(tb) + 1, buf = npv & 1;
-          ok = wait(sh, &sh.full[st], S::parity(tb)) && wait(sh, &sh.pready[s][buf], (npv >> 1) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const bool last = hb == 1 || keys_of(w, base + tb) <= kHalf;
-          tc_fence_after();
-          if (issuer) {
-            const uint64_t db = vdesc + st * kStep + hb * kHalfStep;
+          if (two) ok = meet(&sh.meet[0]);
+          if (ok && tiles > 0) ok = __all_sync(0xffffffffu, wait(sh, &sh.qfull[s], (nq - 1) & 1));
+          for (int i = 0; ok && i < tiles; ++i, t += stride, j += stride) {
+            const int st = S::stage(t), halves = keys_of(w, j) > kHalf ? 2 : 1;
+            ok = __all_sync(0xffffffffu, wait(sh, &sh.full[st], S::parity(t)));
+            for (int h = 0; ok && h < halves; ++h) {
+              const int buf = n & 1;
+              ok = n < 2 || __all_sync(0xffffffffu, wait(sh, &sh.pvdone[s][buf], ((n >> 1) - 1) & 1));
+              if (!ok) break;
+              tc_fence_after();
+              if (issuer) {
+                const uint64_t db = kdesc + st * kStep + h * kHalfStep;
 #pragma unroll
-            for (int q = 0; q < kHalf / 16; ++q)
-              mma_ts(o_at, s_at + buf * kHalf + q * 8, db + q * (2048 >> 4), idesc_o, q > 0 || !fresh);
-            mma_commit(&sh.pvdone[s][buf]);
-            if (last) {
-              mma_commit(&sh.empty[st]);
-              if (!two) mma_commit(&sh.empty[st]);
+                for (int k = 0; k < DP / 16; ++k) {
+                  const int off = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
+                  if (k < ksteps) mma_ss(s_at + buf * kHalf, qdesc + off, db + off, idesc, k > 0);
+                }
+                mma_commit(&sh.sfull[s][buf]);
+                if (h == halves - 1) {
+                  mma_commit(&sh.empty[st]);
+                  if (!two) mma_commit(&sh.empty[st]);  // (the other group's share)
+                }
+              }
+              __syncwarp();
+              ++n;
             }
           }
-          __syncwarp();
-          ++npv;
-          hb ^= 1;
-          if (last) {
-            hb = 0;
-            tb += stride;
-            --kb;
-          }
-          // (the softmax of the step in between is under way meanwhile)
-          if (ka > 0) ok = scores();
+          t0 += w.j1 - w.j0;
+          more = ok && next_part();
         }
-        // the part's last S is done: its query tile can go
-        more = ok && next_part();
-        if (more && tiles_of(w, t0)) load_q(w);
+        if (!ok) {  // let the copy in flight end
+          const uint64_t ts = global_ns();
+          while (nq > 0 && !mbar_try_wait(&sh.qfull[s], (nq - 1) & 1) && global_ns() - ts < kWaitLimitNs) {
+          }
+        }
+      } else {
+        // O += P V
+        constexpr uint32_t idesc = instr_desc(kBf16, DP, true);
+        const uint64_t vdesc = smem_desc(smem_addr(ring), kTile * 128);
+        uint32_t nown = 0;  // parts with tiles of this group so far
+        while (ok && more) {
+          const bool two = w.two;
+          const int tiles = tiles_of(), stride = two ? 1 : 2;
+          int t = two ? t0 : t0 + ((s ^ t0) & 1), j = w.j0 + t - t0;
+          if (two) ok = meet(&sh.meet[1]);
+          if (ok && tiles > 0 && nown++ > 0) ok = __all_sync(0xffffffffu, wait(sh, &sh.oempty[s], (nown - 2) & 1));
+          for (int i = 0; ok && i < tiles; ++i, t += stride, j += stride) {
+            const int st = S::stage(t) + 1, halves = keys_of(w, j) > kHalf ? 2 : 1;
+            ok = __all_sync(0xffffffffu, wait(sh, &sh.full[st], S::parity(t)));
+            for (int h = 0; ok && h < halves; ++h) {
+              const int buf = n & 1;
+              ok = __all_sync(0xffffffffu, wait(sh, &sh.pready[s][buf], (n >> 1) & 1));
+              if (!ok) break;
+              tc_fence_after();
+              if (issuer) {
+                const uint64_t db = vdesc + st * kStep + h * kHalfStep;
+#pragma unroll
+                for (int q = 0; q < kHalf / 16; ++q)
+                  mma_ts(o_at, s_at + buf * kHalf + q * 8, db + q * (2048 >> 4), idesc, q > 0 || h > 0 || i > 0);
+                mma_commit(&sh.pvdone[s][buf]);
+                if (h == halves - 1) {
+                  mma_commit(&sh.empty[st]);
+                  if (!two) mma_commit(&sh.empty[st]);
+                }
+              }
+              __syncwarp();
+              ++n;
+            }
+          }
+          t0 += w.j1 - w.j0;
+          more = ok && next_part();
+        }
       }
-      if (!ok) {  // let the products and the copy in flight end
-        if (issuer) mma_commit(&sh.drain[s]);
+      if (!ok) {  // let the products in flight end
+        if (issuer) mma_commit(&sh.drain[warp - kWarpS]);
         const uint64_t ts = global_ns();
-        while (!mbar_try_wait(&sh.drain[s], 0) && global_ns() - ts < kWaitLimitNs) {
-        }
-        while (nq > 0 && !mbar_try_wait(&sh.qfull[s], (nq - 1) & 1) && global_ns() - ts < kWaitLimitNs) {
+        while (!mbar_try_wait(&sh.drain[warp - kWarpS], 0) && global_ns() - ts < kWaitLimitNs) {
         }
       }
       __syncwarp();
@@ -895,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       }
     }
   }
-  if (warp == kWarpMma)
+  if (warp == kWarpS)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
