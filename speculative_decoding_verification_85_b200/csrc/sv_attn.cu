@@ -166,24 +166,22 @@ struct Shared {
   Part parts[kParts];
 };
 
-// Wait for a phase; false once any wait of the CTA has run out of time.
-__device__ __forceinline__ bool wait_long(Shared& sh, uint64_t* bar, uint32_t parity) {
+// Wait for a phase; false once any wait of the CTA has run out of time.  (Kept
+// short: it is inlined at every wait, and instruction fetches are part of what
+// this kernel waits for.)
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
-  for (;;) {
-    for (int k = 0; k < 64; ++k)
-      if (mbar_try_wait(bar, parity)) return true;
-    volatile int* dead = &sh.dead;
+  volatile int* dead = &sh.dead;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
     if (*dead) return false;
     if (global_ns() - t0 > kWaitLimitNs) {
       *dead = 1;
       return false;
     }
   }
-}
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
-  for (int k = 0; k < 16; ++k)
-    if (mbar_try_wait(bar, parity)) return true;
-  return wait_long(sh, bar, parity);
+  return true;
 }
 
 template <bool kBf16>
