@@ -212,10 +212,14 @@ def kv_slots(lens, add, cu_rows, block_table, free_pages, free_count, *, rows: i
         _want(dev, (path, "path", torch.int32, (B, width), True))
 
     def body(s):
-        slots = _out(out_slots, "out_slots", torch.int32, (rows,), dev)
-        start = _out(out_start, "out_start", torch.int32, (B,), dev)
-        new = _out(out_lens, "out_lens", torch.int32, (B,), dev)
-        count = _out(out_free_count, "out_free_count", torch.int32, (1,), dev)
+        if out_slots is out_start is out_lens is out_free_count is None:  # one allocation
+            slots, start, new, count = torch.empty(
+                rows + 2 * B + 1, dtype=torch.int32, device=dev).split((rows, B, B, 1))
+        else:
+            slots = _out(out_slots, "out_slots", torch.int32, (rows,), dev)
+            start = _out(out_start, "out_start", torch.int32, (B,), dev)
+            new = _out(out_lens, "out_lens", torch.int32, (B,), dev)
+            count = _out(out_free_count, "out_free_count", torch.int32, (1,), dev)
         _check(_lib().spec_kv_slots(
             _p(lens), _p(add), _p(cu_rows), _p(path), width, _p(block_table),
             block_table.stride(0) if B > 1 else W, W, _p(free_pages), pool, _p(free_count), B,
