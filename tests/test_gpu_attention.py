@@ -306,3 +306,16 @@ def test_nothing_to_do():
     sv.tree_attention(**dict(st, cu_nodes=i32([0]), lens=st["lens"][:0],
                              block_table=st["block_table"][:0]), out=out)
     assert (out == 2).all()
+
+
+def test_pages_beyond_32_bit_offsets():
+    """A cache of more than 2^31 elements, its last pages in use."""
+    st = make([300], [9], 8, 2, 128, 16, "bf16", seed=18)
+    pages = 2**31 // (16 * 2 * 128) + 64
+    kc, vc = (torch.empty(pages, 16, 2, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    n = st["k_cache"].shape[0]
+    kc[-n:], vc[-n:] = st["k_cache"], st["v_cache"]
+    want, _ = check(st)
+    out, _ = sv.tree_attention(**dict(st, k_cache=kc, v_cache=vc,
+                                      block_table=st["block_table"] + (pages - n)))
+    assert torch.equal(out, want)

@@ -179,3 +179,17 @@ def test_append_strided():
             want[s // page, 1, :, s % page] = v[i]
         sv.kv_append(k, v, slots.to(DEV, torch.int32), kc, vc)
         assert torch.equal(both, want)
+
+
+def test_append_beyond_32_bit_offsets():
+    """Layers of more than 2^31 elements in all; the last layer's last slots."""
+    H, D, page = 2, 128, 16
+    pages = 2**30 // (page * H * D) + 3
+    kc, vc = (torch.zeros(2, pages, page, H, D, dtype=torch.uint8, device=DEV) for _ in range(2))
+    k, v = (torch.randint(1, 255, (2, 3, H, D), dtype=torch.uint8, device=DEV) for _ in range(2))
+    slots = [pages * page - 1, 5, pages * page - 17]
+    sv.kv_append(k, v, i32(slots), kc, vc)
+    for i, s in enumerate(slots):
+        assert torch.equal(kc[:, s // page, s % page], k[:, i])
+        assert torch.equal(vc[:, s // page, s % page], v[:, i])
+    assert int((kc != 0).any(-1).sum()) == 2 * 3 * H

@@ -214,3 +214,20 @@ def test_no_sequences():
     e = dict(st, cu_nodes=st["cu_nodes"][:1], draw_uniforms=st["draw_uniforms"][:0])
     acc, tok, path = sv.spec_verify_tree(**e, max_nodes=3)
     assert acc.shape == (0,) and tok.shape == (0, 3) and path.shape == (0, 3)
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Probabilities of more than 2^31 elements, the last rows in use."""
+    V, n = 151936, 5
+    st = make(2, [n], V, "bf16", "chain", seed=51)
+    rows = 2**31 // V + 2 * n + 1
+    big = {}
+    for k in ("target", "draft"):
+        big[k] = torch.empty(rows, V, dtype=torch.bfloat16, device=DEV)
+        big[k][-2 * n:] = st[k]
+    for k in ("tokens", "parents", "uniforms"):
+        big[k] = torch.zeros(rows, dtype=st[k].dtype, device=DEV)
+        big[k][-2 * n:] = st[k]
+    got = run(dict(st, **big, cu_nodes=st["cu_nodes"] + (rows - 2 * n)), n)
+    for g, w in zip(got, ref(st, n)):
+        assert np.array_equal(g, w)
