@@ -88,7 +88,7 @@ struct alignas(64) AttnParams {
   int B, N, Hq, Hkv, G, D, num_pages, page, width;
   int box;             // tokens of one load from a page
   int npt;             // nodes of one query tile
-  int ctas;
+  int ctas, groups;    // CTAs; column groups of four of a partial result
   float sl;            // scale * log2(e)
   float* part_o;       // partial results: [cta][2][tile][DP / 4][128][4]
   float2* part_s;      // [cta][2][tile][128] (shift, sum)
@@ -344,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   if (!few) find_start(std::true_type());
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;");
   const uint32_t tmem = sh.tmem;
   // Part `seg`; every reader takes them all, in order, and gives each back (freed).
   // Keys of tile j of a unit; a tile of more than kHalf takes two steps.
@@ -903,11 +902,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 }
 
 // Join of the units that CTA borders cut.  Every block lists the cut units
-// (one for each CTA at most) and takes its share of their items: 32 rows by
-// one group of four columns, the parts dealt to the block's eight warps, when
-// the unit has eight parts or more, else 32 rows by eight column groups, one
-// a warp.  Parts are added in a fixed order.
+// (one for each CTA at most) and takes its share of their items: 32 rows, a
+// warp an eighth of the columns, or, where a unit has eight parts or more, 32
+// rows by one group of four columns, a warp an eighth of the parts.  Bound by
+// the parts' bytes, so a lane has several loads in flight; parts are added in a
+// fixed order.
 constexpr int kJoinThreads = 256;
+
+// Adds parts p, p + step, ... (kAt of them at a time, loaded together) of kGroups column groups;
+// the shift follows the largest so far.
+template <int kGroups, int kAt, typename Row>
+__device__ __forceinline__ void join_parts(const AttnParams& P, Row row_of, int p, int parts, int step, int r,
+                                           int cg, float& top, float& sum, float4 (&o)[kGroups]) {
+  for (; p < parts; p += kAt * step) {
+    float2 s[kAt];
+    float4 x[kAt][kGroups];
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) {
+      s[i] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) x[i][g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (p + i * step < parts) {
+        const int64_t tile = row_of(p + i * step);  // tile of the partial results
+        s[i] = P.part_s[tile * kTile + r];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+          x[i][g] = reinterpret_cast<const float4*>(P.part_o)[(tile * P.groups + cg + g) * kTile + r];
+      }
+    }
+    float now = top;
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) now = fmaxf(now, s[i].x);
+    const float f0 = top == -INFINITY ? 0.0f : ex2_approx(top - now);
+    top = now;
+    sum *= f0;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) o[g] = make_float4(o[g].x * f0, o[g].y * f0, o[g].z * f0, o[g].w * f0);
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) {
+      const float f = s[i].x == -INFINITY ? 0.0f : ex2_approx(s[i].x - top);
+      sum += f * s[i].y;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        o[g].x += f * x[i][g].x;
+        o[g].y += f * x[i][g].y;
+        o[g].z += f * x[i][g].z;
+        o[g].w += f * x[i][g].w;
+      }
+    }
+  }
+}
+
 template <int DP, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ AttnParams P) {
   __shared__ int first[kJoinThreads];   // first item behind each unit
@@ -916,6 +961,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
   __shared__ int wsum[8];
   __shared__ float4 acc_s[8][32];
   __shared__ float2 st_s[8][32];
+  constexpr int kGroups = DP / 32;  // column groups of a warp where it has all parts
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int last_row = P.npt * P.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -926,7 +972,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
     unit[tid] = d;
     parts_s[tid] = parts;
     const int blocks = d.y == 0 ? 0 : d.y > P.npt ? 4 + cdiv((d.y - P.npt) * P.G, 32) : cdiv(d.y * P.G, 32);
-    items = blocks * (parts >= 8 ? DP / 4 : DP / 32);
+    items = blocks * (parts >= 8 ? DP / 4 : 1);
   }
   int incl = items;
 #pragma unroll
@@ -955,74 +1001,55 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
     const int parts = parts_s[cta];
     const int k = item - (cta > 0 ? first[cta - 1] : 0);
     const bool split = parts >= 8;
-    const int cgs = split ? DP / 4 : DP / 32;
-    const int rb = k / cgs, cg = split ? k - rb * cgs : (k - rb * cgs) * 8 + warp;
+    const int rb = split ? k / (DP / 4) : k;
     const int tile = rb >> 2, r = (rb & 3) * 32 + lane;
     const int rnode = r / P.G, rg = r - rnode * P.G;
     const bool mine = r < last_row && tile * P.npt + rnode < d.y;
+    const int64_t row = static_cast<int64_t>(d.x + tile * P.npt + rnode) * P.Hq + d.z * P.G + rg;
     auto at = [&](int p) { return static_cast<int64_t>((p == 0 ? d.w : (cta + p) * 2) * 2 + tile); };
-    float top = -INFINITY, sum = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (mine) {
-      // four parts at a time, loaded together; the shift follows the largest so far
-      const int step = split ? 8 : 1;
-      for (int p = split ? warp : 0; p < parts; p += 4 * step) {
-        float2 s[4];
-        float4 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[i] = make_float2(-INFINITY, 0.0f);
-          x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (p + i * step < parts) {
-            s[i] = P.part_s[at(p + i * step) * kTile + r];
-            x[i] = reinterpret_cast<const float4*>(P.part_o)[(at(p + i * step) * (DP / 4) + cg) * kTile + r];
-          }
-        }
-        const float now = fmaxf(top, fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x)));
-        const float g = top == -INFINITY ? 0.0f : ex2_approx(top - now);
-        top = now;
-        sum *= g;
-        o = make_float4(o.x * g, o.y * g, o.z * g, o.w * g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = s[i].x == -INFINITY ? 0.0f : ex2_approx(s[i].x - top);
-          sum += f * s[i].y;
-          o.x += f * x[i].x;
-          o.y += f * x[i].y;
-          o.z += f * x[i].z;
-          o.w += f * x[i].w;
-        }
-      }
-    }
-    if (split) {
-      acc_s[warp][lane] = o;
-      st_s[warp][lane] = make_float2(top, sum);
-      __syncthreads();
-      if (warp == 0) {
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, st_s[i][lane].x);
-        sum = 0.0f;
-        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int i = 0; i < 8; ++i) {
-          const float2 s = st_s[i][lane];
-          const float4 x = acc_s[i][lane];
-          const float f = s.x == -INFINITY ? 0.0f : ex2_approx(s.x - top);
-          sum += f * s.y;
-          o.x += f * x.x;
-          o.y += f * x.y;
-          o.z += f * x.z;
-          o.w += f * x.w;
-        }
-      }
-    }
-    if (mine && (!split || warp == 0)) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int64_t row = static_cast<int64_t>(d.x + tile * P.npt + rnode) * P.Hq + d.z * P.G + rg;
+    auto write = [&](int cg, float4 o, float inv) {
       if (cg * 4 < P.D)
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + row * P.D + cg * 4) =
             make_uint2(pack2<kBf16>(o.x * inv, o.y * inv), pack2<kBf16>(o.z * inv, o.w * inv));
+    };
+    float top = -INFINITY, sum = 0.0f;
+    if (!split) {
+      float4 o[kGroups] = {};
+      const int cg = warp * kGroups;
+      if (mine) {
+        join_parts<kGroups, 2>(P, at, 0, parts, 1, r, cg, top, sum, o);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) write(cg + g, o[g], inv);
+        if (P.lse && warp == 0) P.lse[row] = (top + log2f(sum)) * kLn2;
+      }
+      continue;
+    }
+    float4 o[1] = {};
+    const int cg = k - rb * (DP / 4);
+    if (mine) join_parts<1, 4>(P, at, warp, parts, 8, r, cg, top, sum, o);
+    acc_s[warp][lane] = o[0];
+    st_s[warp][lane] = make_float2(top, sum);
+    __syncthreads();
+    if (warp == 0 && mine) {
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, st_s[i][lane].x);
+      sum = 0.0f;
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int i = 0; i < 8; ++i) {
+        const float2 s = st_s[i][lane];
+        const float4 x = acc_s[i][lane];
+        const float f = s.x == -INFINITY ? 0.0f : ex2_approx(s.x - top);
+        sum += f * s.y;
+        y.x += f * x.x;
+        y.y += f * x.y;
+        y.z += f * x.z;
+        y.w += f * x.w;
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      write(cg, y, inv);
       if (P.lse && cg == 0) P.lse[row] = (top + log2f(sum)) * kLn2;
     }
-    if (split) __syncthreads();
+    __syncthreads();
   }
 }
 
@@ -1229,6 +1256,7 @@ int spec_tree_attention(const sv_tree_attention_args* a, void* workspace, size_t
   p.box = box;
   p.npt = npt;
   p.ctas = ctas;
+  p.groups = (a->D <= 64 ? 64 : 128) / 4;
   p.sl = a->scale * kLog2e;
   char* ws = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws + lay.o);
