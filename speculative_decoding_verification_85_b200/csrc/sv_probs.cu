@@ -448,12 +448,15 @@ __global__ void __launch_bounds__(kPThreads) probs_kernel(const __grid_constant_
 template <bool kBf16>
 int launch_probs(ProbsParams p, int B, cudaStream_t stream) {
   const int nch = static_cast<int>((static_cast<int64_t>(p.V) + kChunk - 1) / kChunk);
-  // Cluster size: one CTA a sequence where the sequences fill the SMs, else enough for four a
-  // SM, with no slice below one chunk a warp.  (256 sequences of V = 151936 fp32: 61 us with
-  // one CTA each, 64 with four; 64 trees of V = 128256 bf16: 56 us with four, 44 with eight.)
+  // Cluster size: as many CTAs as run at once (three a SM), so that none waits for a second
+  // wave; trees with draft laws, which take sum after sum from the same rows, gain from more
+  // CTAs even so.  No slice is below one chunk a warp.  (V = 151936 fp32 chains: 64 sequences
+  // 21 us with four CTAs each, 26 with eight; 128: 34 with two, 39 with four; 256: 59 with one,
+  // 64 with two.  V = 128256 bf16 trees of 21 nodes: 64 sequences 36 us with eight, 46 with four;
+  // 128: 57 with eight, 63 with four.)
+  const int limit = (p.tree && p.draft ? 8 : 3) * 148;
   int C = 1;
-  if (B < 148)
-    while (C < kMaxCluster && B * C < 4 * 148 && nch > C * kPWarps) C *= 2;
+  while (C < kMaxCluster && B * C * 2 <= limit && nch > C * kPWarps) C *= 2;
   p.cluster = C;
   p.chunks = (nch + C - 1) / C;
   const int cap = p.tree ? (p.width < SV_MAX_NODES ? p.width : SV_MAX_NODES) : p.gamma + 1;
