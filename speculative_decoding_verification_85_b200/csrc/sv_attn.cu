@@ -24,12 +24,12 @@
 // accumulated, which fp32 holds as well.
 //
 // Bound by memory up to about 250 query rows a key head.  Measured (1.08 GB of
-// keys and values, 64 x 4096 tokens, 8 key heads of 128, pages of 128): 182 us
-// with 4 rows a key head (0.90 of the measured copy bandwidth), 210 us with
-// 128, 333 us with 256 (two groups of 128 exponentials a key each): there the
+// keys and values, 64 x 4096 tokens, 8 key heads of 128, pages of 128): 176 us
+// with 4 rows a key head (0.93 of the measured copy bandwidth), 201 us with
+// 128, 314 us with 256 (two groups of 128 exponentials a key each): there the
 // chain scores -> weights -> accumulator -> next scores of a group sets the
-// pace, at 46% of the tensor pipe and of the special function units.  Pages of
-// 16 cost 9% more than pages of 128 (eight loads a tile).
+// pace, at half of the tensor pipe and of the special function units.  Pages of
+// 16 cost 10% more than pages of 128 (eight loads a tile).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
