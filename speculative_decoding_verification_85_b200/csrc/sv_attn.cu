@@ -11,7 +11,7 @@
 // results (unnormalised output, exponent shift, sum) in the workspace and
 // combine_kernel joins them in a fixed order.
 //
-// One CTA: two warps fill a ring of key and value tiles by TMA; two groups of
+// One CTA: four warps fill a ring of key and value tiles by TMA; two groups of
 // four softmax warps turn scores S = Q K^T (fp32, tensor memory) into weights P
 // (a thread a row: maximum, exponentials and sum need no exchange), each fed by
 // one warp that issues its S and one that issues its O += P V.  With two query
@@ -29,7 +29,8 @@
 // 128, 314 us with 256 (two groups of 128 exponentials a key each): there the
 // chain scores -> weights -> accumulator -> next scores of a group sets the
 // pace, at half of the tensor pipe and of the special function units.  Pages of
-// 16 cost 10% more than pages of 128 (eight loads a tile).
+// 16 cost 4% more than pages of 128 (eight loads a tile and 64 columns; 9% with
+// one loading warp for both column halves).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -50,9 +51,10 @@ constexpr int kHalf = 64;           // keys of a step
 constexpr int kWarpsSoft = 8;       // softmax warps: two groups of four
 // Warps 0-7: softmax; 8: keys, 9: values; 10 and 11: first products of each
 // softmax group; 12 and 13: second products (apart, since each would wait for
-// the other's turn).
-constexpr int kWarpV = 9, kWarpS = 10, kWarpO = 12;
-constexpr int kThreads = 32 * 16;     // (the last two warps only fill their warpgroup)
+// the other's turn); 14 and 15: keys and values beyond the first 64 columns of
+// a head (small pages are many loads).
+constexpr int kWarpK = 8, kWarpS = 10, kWarpO = 12, kWarpMore = 14;
+constexpr int kThreads = 32 * 16;
 // Registers: the softmax groups hold 64 scores a thread, the others need few.
 // 2 x 168 + 2 x 88 = 4 x 128, what a block of 512 threads is launched with.
 constexpr int kRegsSoft = 168, kRegsRest = 88;
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
   if (tid == 0) {
     for (int i = 0; i < 2 * S::kPairs; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], S::kHalves);  // a loading warp for each 64 columns
       mbar_init(&sh.empty[i], 2);  // both groups' products
     }
     for (int i = 0; i < 2; ++i) {
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     mbar_init(&sh.met, kWarpsSoft);
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&sh.parted[i], 1);
-      mbar_init(&sh.freed[i], kWarpsSoft + 5);  // softmax, values and products
+      mbar_init(&sh.freed[i], kWarpsSoft + 2 * S::kHalves - 1 + 4);  // softmax, loads but the first, products
     }
     for (int i = 0; i < 4; ++i) sh.badv[i] = 0;
     mbar_init_fence();
@@ -363,23 +365,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
   if (warp >= kWarpsSoft) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp < kWarpS) {
+    if (warp < kWarpS || (S::kHalves == 2 && warp >= kWarpMore)) {
       // -------------------------------------------------- keys and values
-      // one warp each
-      const bool kv = warp == kWarpV;
+      // a warp for each and for each 64 columns of a head; the first one also walks the line
+      const bool kv = warp & 1, lead = warp == kWarpK;
+      const int hf = warp >= kWarpMore;
       const CUtensorMap* own = kv ? &P.vmap : &P.kmap;
       const CUtensorMap* cached = kv ? &P.vcmap : &P.kcmap;
       int t = 0, seg = 0;
       bool ok = true;
       Walk walk{};
-      if (!kv) {
+      if (lead) {
         if (few) find_start(std::false_type());
         __syncwarp();
         walk = sh.start;
       }
       for (;; ++seg) {
         Part w;
-        if (kv) {
+        if (!lead) {
           if (!part_of(seg, w)) break;
           if (lane == 0) mbar_arrive(&sh.freed[seg % kParts]);
         } else {
@@ -417,25 +420,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           const int rows = tree ? kTreeBox : P.box;
           const int boxes = (valid + rows - 1) / rows;
           if (page < 0 || page >= P.num_pages) {
-            if (!kv) sh.badpage[seg % kParts] = 1;  // the rows will be marked
+            if (lead) sh.badpage[seg % kParts] = 1;  // the rows will be marked
             page = 0;
           }
           const int st = S::stage(t) + (kv ? 1 : 0);
           ok = __all_sync(0xffffffffu, wait(sh, &sh.empty[st], S::parity(t) ^ 1));
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], boxes * rows * 128 * S::kHalves);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], boxes * rows * 128);
           __syncwarp();
           if (lane < boxes) {
-            char* dst = ring + st * S::kTileBytes + lane * rows * 128;
+            char* dst = ring + st * S::kTileBytes + hf * (kTile * 128) + lane * rows * 128;
             if (tree) {
-#pragma unroll
-              for (int hf = 0; hf < S::kHalves; ++hf)
-                tma_3d(dst + hf * (kTile * 128), own, hf * 64, w.h, w.lo + c * kTile + lane * kTreeBox, &sh.full[st]);
+              tma_3d(dst, own, hf * 64, w.h, w.lo + c * kTile + lane * kTreeBox, &sh.full[st]);
             } else {
               const int tok = span == 1 ? 0 : (c % span) * kTile;
-#pragma unroll
-              for (int hf = 0; hf < S::kHalves; ++hf)
-                tma_4d(dst + hf * (kTile * 128), cached, hf * 64, tok, w.h, page, &sh.full[st]);
+              tma_4d(dst, cached, hf * 64, tok, w.h, page, &sh.full[st]);
             }
           }
           __syncwarp();
@@ -444,15 +444,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         }
         if (!ok) break;
       }
-      if (!ok) {  // leave no copy in flight behind
-        for (int i = max(0, t - S::kPairs); i < t; ++i) {
-          const uint64_t t0 = global_ns();
-          while (!mbar_try_wait(&sh.full[S::stage(i) + (kv ? 1 : 0)], S::parity(i)) && global_ns() - t0 < kWaitLimitNs) {
-          }
+      // leave no copy in flight behind (the others may have given up)
+      for (int i = max(0, t - S::kPairs); i < t; ++i) {
+        const uint64_t t0 = global_ns();
+        while (!mbar_try_wait(&sh.full[S::stage(i) + (kv ? 1 : 0)], S::parity(i)) && global_ns() - t0 < kWaitLimitNs) {
         }
       }
       __syncwarp();
-    } else if (warp < kWarpO + 2) {
+    } else if (warp < kWarpMore) {
       // --------------------------------------------------------- products
       // a warp for each kind and softmax group; the whole warp keeps the books, one lane issues
       const int s = (warp - kWarpS) & 1;
@@ -536,10 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           t0 += w.j1 - w.j0;
           more = ok && next_part();
         }
-        if (!ok) {  // let the copy in flight end
-          const uint64_t ts = global_ns();
-          while (nq > 0 && !mbar_try_wait(&sh.qfull[s], (nq - 1) & 1) && global_ns() - ts < kWaitLimitNs) {
-          }
+        const uint64_t ts = global_ns();  // the copy in flight, if any
+        while (nq > 0 && !mbar_try_wait(&sh.qfull[s], (nq - 1) & 1) && global_ns() - ts < kWaitLimitNs) {
         }
       } else {
         // O += P V
@@ -579,11 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           more = ok && next_part();
         }
       }
-      if (!ok) {  // let the products in flight end
-        if (issuer) mma_commit(&sh.drain[warp - kWarpS]);
-        const uint64_t ts = global_ns();
-        while (!mbar_try_wait(&sh.drain[warp - kWarpS], 0) && global_ns() - ts < kWaitLimitNs) {
-        }
+      // the products in flight
+      if (issuer) mma_commit(&sh.drain[warp - kWarpS]);
+      const uint64_t ts = global_ns();
+      while (!mbar_try_wait(&sh.drain[warp - kWarpS], 0) && global_ns() - ts < kWaitLimitNs) {
       }
       __syncwarp();
     }
