@@ -11,7 +11,8 @@
 // 512 entries (one warp a chunk, 16 entries a lane in flight), the slices'
 // sums are exchanged through distributed shared memory, every CTA finds the
 // slice that the uniform falls into, and one warp of that CTA walks down its
-// chunk sums and one chunk again (from L2).  Sums are fp64: the order of
+// chunk sums and one chunk again (from L2).  256 chains of 4 at V = 151936 fp32
+// take 53 us: 0.86 of the measured copy bandwidth.  Sums are fp64: the order of
 // addition then moves a border by 1e-16 of the mass, so the drawn entry is
 // the one of the definition.
 #include <cuda_runtime.h>
@@ -74,38 +75,44 @@ __device__ __forceinline__ int chunk_entry(int e, int lane) {
   return kBf16 ? 256 * (e >> 3) + 8 * lane + (e & 7) : 128 * (e >> 2) + 4 * lane + (e & 3);
 }
 
-// This lane's 16 entries of the chunk starting at entry v of a row; entries
-// from `end` on are 0.  A whole chunk of a 16-byte aligned row is four (bf16:
-// two) 16-byte loads, anything else 16 element loads, a warp's consecutive.
+// This lane's 16 entries of the whole chunk starting at entry v of a 16-byte
+// aligned row: four (bf16: two) 16-byte loads.
+template <bool kBf16>
+__device__ __forceinline__ void load_whole(const void* row, int v, int lane, float (&x)[16]) {
+  if constexpr (kBf16) {
+    const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + v);
+    uint4 w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) w[k] = __ldg(g + 32 * k + lane);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t r[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[8 * k + 2 * i] = bf16_lo(r[i]);
+        x[8 * k + 2 * i + 1] = bf16_hi(r[i]);
+      }
+    }
+  } else {
+    const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(row) + v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 w = __ldg(g + 32 * k + lane);
+      x[4 * k] = w.x;
+      x[4 * k + 1] = w.y;
+      x[4 * k + 2] = w.z;
+      x[4 * k + 3] = w.w;
+    }
+  }
+}
+
+// The same for any chunk; entries from `end` on are 0.  One that is not whole
+// or not aligned is 16 element loads, a warp's consecutive.
 template <bool kBf16>
 __device__ __forceinline__ void load_chunk(const void* row, int v, int end, int lane, bool vec,
                                            float (&x)[16]) {
   if (vec && v + kChunk <= end) {
-    if constexpr (kBf16) {
-      const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + v);
-      uint4 w[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) w[k] = __ldg(g + 32 * k + lane);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t r[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[8 * k + 2 * i] = bf16_lo(r[i]);
-          x[8 * k + 2 * i + 1] = bf16_hi(r[i]);
-        }
-      }
-    } else {
-      const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(row) + v);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 w = __ldg(g + 32 * k + lane);
-        x[4 * k] = w.x;
-        x[4 * k + 1] = w.y;
-        x[4 * k + 2] = w.z;
-        x[4 * k + 3] = w.w;
-      }
-    }
+    load_whole<kBf16>(row, v, lane, x);
   } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
@@ -118,7 +125,7 @@ __device__ __forceinline__ void load_chunk(const void* row, int v, int end, int 
 // Shared memory behind ProbsShared: chunk sums [chunks] fp64, then per node
 // p, q, u (fp32) and token, parent, path, rejected-token list (int).
 template <bool kBf16>
-__global__ void __launch_bounds__(kPThreads) probs_kernel(const __grid_constant__ ProbsParams P) {
+__global__ void __launch_bounds__(kPThreads, 3) probs_kernel(const __grid_constant__ ProbsParams P) {
   extern __shared__ __align__(16) char smem[];
   __shared__ ProbsShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -237,7 +244,29 @@ __global__ void __launch_bounds__(kPThreads) probs_kernel(const __grid_constant_
   // The mass of that law over the whole row: chunk sums into csum, the
   // slices' sums into every CTA's xsum.  The same bits in every CTA.
   auto reduce = [&](int cur, double c, int ngone) {
-    for (int k = warp; k < P.chunks; k += kPWarps) {
+    // Whole chunks of aligned row pairs, two of them at a time, all loads first: a CTA that has a
+    // row pair to itself is bound by what it has in flight.
+    const char* pr = tgt + (trow + cur) * rowbytes;
+    const char* qr = c != 0.0 ? drf + (drow + cur) * rowbytes : pr;
+    const bool vec = c != 0.0 && reinterpret_cast<uintptr_t>(pr) % 16 == 0 && reinterpret_cast<uintptr_t>(qr) % 16 == 0;
+    int k = warp;
+    for (; vec && v0 + (k + kPWarps + 1) * kChunk <= v1; k += 2 * kPWarps) {
+      float p[2][16], q[2][16];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        load_whole<kBf16>(pr, v0 + (k + i * kPWarps) * kChunk, lane, p[i]);
+        load_whole<kBf16>(qr, v0 + (k + i * kPWarps) * kChunk, lane, q[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        double s = 0.0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s += weight(p[i][e], c, q[i][e]);
+        s = warp_sum(s);
+        if (lane == 0) csum[k + i * kPWarps] = s;
+      }
+    }
+    for (; k < P.chunks; k += kPWarps) {
       const int v = v0 + k * kChunk;
       double s = 0.0;
       if (v < v1) {
@@ -451,9 +480,9 @@ int launch_probs(ProbsParams p, int B, cudaStream_t stream) {
   // Cluster size: as many CTAs as run at once (three a SM), so that none waits for a second
   // wave; trees with draft laws, which take sum after sum from the same rows, gain from more
   // CTAs even so.  No slice is below one chunk a warp.  (V = 151936 fp32 chains: 64 sequences
-  // 21 us with four CTAs each, 26 with eight; 128: 34 with two, 39 with four; 256: 59 with one,
-  // 64 with two.  V = 128256 bf16 trees of 21 nodes: 64 sequences 36 us with eight, 46 with four;
-  // 128: 57 with eight, 63 with four.)
+  // 20 us with four CTAs each, 25 with eight; 128: 30 with two, 37 with four; 256: 53 with one,
+  // 61 with two.  V = 128256 bf16 trees of 21 nodes: 64 sequences 31 us with eight, 32 with four,
+  // 45 with two.)
   const int limit = (p.tree && p.draft ? 8 : 3) * 148;
   int C = 1;
   while (C < kMaxCluster && B * C * 2 <= limit && nch > C * kPWarps) C *= 2;
