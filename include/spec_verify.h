@@ -16,6 +16,9 @@
  *                          Algorithm 1.
  *   spec_verify_shard_*    spec_verify for logits split over the vocabulary
  *                          across ranks (spec_verify_shard.h).
+ *   spec_verify_probs, spec_verify_tree, spec_tree_attention, spec_kv_*
+ *                          drafted trees over a paged cache, verified from
+ *                          given probabilities (spec_tree.h).
  *
  * Conventions shared by every entry point
  *   - Logit tensors are dense, row-major, contiguous, in device memory, fp32
