@@ -360,6 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     o[0] = d[0];
     o[1] = d[1];
     o[2] = d[2];
+    // one lane gives the place back for the whole warp: not before every lane has read it
+    __syncwarp();
     return w.b >= 0;
   };
 
