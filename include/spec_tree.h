@@ -196,7 +196,9 @@ int spec_kv_append(const sv_kv_append_args* args, void* stream);
  * SV_MAX_HEAD_DIM, Hq a multiple of Hkv, Hq / Hkv <= 128; page_size 8, 16,
  * 32, 64 or a multiple of 128; strides (elements) multiples of 8, addresses
  * 16-byte aligned.  Products are accumulated in fp32, the softmax is fp32,
- * its weights are rounded to the input type for the second product.
+ * its weights are rounded to the input type for the second product: by 2^-8
+ * (bf16) or 2^-11 (fp16) of themselves, in fp16 also by up to 2^-32 of their
+ * row's largest.
  * Nothing a node may not see reaches its result, whatever it holds (other
  * branches, rest of the last page, neighbours' rows: infinities and NaN too).
  * Marks: a sequence whose lens is negative or beyond its table row, which

@@ -20,8 +20,8 @@
 // accumulator: same lanes).  A step is 64 keys, and a group has two score
 // buffers: while it weighs one step, the next step's scores are made and the
 // last one's weights used.  The accumulator is rescaled only when a row's
-// maximum has grown by more than 2^8; until then weights up to 2^8 are
-// accumulated, which fp32 holds as well.
+// maximum has grown by more than 2^8; until then weights up to 2^8 (fp16: 2^15,
+// see kHold) are accumulated, which fp32 holds as well.
 //
 // Bound by memory up to about 250 query rows a key head.  Measured (1.08 GB of
 // keys and values, 64 x 4096 tokens, 8 key heads of 128, pages of 128): 176 us
@@ -59,6 +59,13 @@ constexpr int kThreads = 32 * 16;
 // 2 x 168 + 2 x 88 = 4 x 128, what a block of 512 threads is launched with.
 constexpr int kRegsSoft = 168, kRegsRest = 88;
 constexpr float kGrow = 8.0f;       // base-2 growth of a maximum that is let stand
+// A row's exponent shift lies this far below its maximum (base 2).  In fp16 weights below 2^-14
+// lose bits and those below 2^-25 vanish; carried 2^7 higher, the largest stays below
+// 2^(7 + kGrow) and one that is 2^-21 of it is still rounded by 2^-11 of itself.  (11 with a
+// growth of 4 costs 2% on 16 trees of 64 nodes, 440 us against 432; 7 with 8 costs nothing.)
+// bf16 has fp32's exponents and needs none.
+template <bool kBf16>
+constexpr float kHold = kBf16 ? 0.0f : 7.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxCtas = 160;         // SMs of a device, with room
 constexpr int kTreeBox = 16;        // rows of one load of the nodes' own keys and values
@@ -609,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int c = 0; c < kHalf; c += 2) mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], x[c]), x[c + 1]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl - kHold<kBf16>;  // the shift it asks for
       if (fresh) {
         shift = top;
       } else if (__any_sync(0xffffffffu, mine && top - shift > kGrow)) {
@@ -634,8 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       uint64_t part[2] = {0, 0};
 #pragma unroll
       for (int c0 = 0; c0 < kHalf; c0 += 32) {
-        // weights rounded to the input type (relative 2^-8 / 2^-11 at most, as the output
-        // itself is, and averaged over the keys); the sum takes them unrounded
+        // weights rounded to the input type, which the second product needs: by 2^-8 (bf16) or
+        // 2^-11 (fp16) relative at most, as the output itself is, and averaged over the keys;
+        // in fp16 by 2^-25 where that is more, 2^-32 of the row's largest or less (kHold).
+        // The sum takes them unrounded.
         uint32_t pk[16];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
