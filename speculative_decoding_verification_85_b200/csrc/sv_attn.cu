@@ -820,12 +820,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           } else {
             tc_wait_ld();
           }
-          if (extra && mine) {  // infinities and NaN among the values this row sees
-            for (int a = node; a >= 0;) {
+          if (extra && mine) {
+            // infinities and NaN among the values this row sees in this part's tiles (one in
+            // another part's tiles is added there: a part without a key of the row weighs
+            // nothing in the join, and 0 * inf is NaN)
+            const int from = max(w.tt - w.j1, 0) * kTile, to = (w.tt - w.j0) * kTile;
+            for (int a = node; a >= from;) {
               const uint16_t* vr = P.v + (w.lo + a) * P.v_node + w.h * P.v_head;
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (c + e < P.D) {
+                if (a < to && c + e < P.D) {
                   const uint32_t x = __ldg(vr + c + e);
                   if (not_finite<kBf16>(x)) o[e] += widen<kBf16>(x);
                 }
