@@ -201,6 +201,8 @@ int spec_kv_append(const sv_kv_append_args* args, void* stream);
  * row's largest.
  * Nothing a node may not see reaches its result, whatever it holds (other
  * branches, rest of the last page, neighbours' rows: infinities and NaN too).
+ * Where all scores that a node sees are -inf, its out is NaN (0 / 0) and its
+ * lse -inf; a score of +inf or NaN makes both NaN.
  * Marks: a sequence whose lens is negative or beyond its table row, which
  * has more than SV_MAX_NODES nodes, or one of whose pages (of those it uses)
  * lies outside [0, num_pages), gets NaN in its rows; so does a node one of

@@ -248,6 +248,10 @@ __device__ __forceinline__ float widen(uint32_t half) {
   return f;
 }
 
+// A row sees itself at least; its sum is zero only where every score it sees is -inf, and its
+// output is 0 / 0 then, whatever the accumulator holds.
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.0f ? NAN : 1.0f / sum; }
+
 template <int DP, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnParams P) {
   using S = Shape<DP>;
@@ -800,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       }
       if (*const_cast<volatile int*>(&sh.badpage[dseg % kParts])) sum = NAN;
       const bool whole = w.j0 == 0 && w.j1 == w.J;
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float inv = inverse(sum);
       const int slot = cta * 2 + (dseg == 0 ? 0 : 1);
       const int row = w.lo + node;
       const int head = w.h * P.G + rg;
@@ -1029,7 +1033,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
       const int cg = warp * kGroups;
       if (mine) {
         join_parts<kGroups, 2>(P, at, 0, parts, 1, r, cg, top, sum, o);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = inverse(sum);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) write(cg + g, o[g], inv);
         if (P.lse && warp == 0) P.lse[row] = (top + log2f(sum)) * kLn2;
@@ -1056,7 +1060,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
         y.z += f * x.z;
         y.w += f * x.w;
       }
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float inv = inverse(sum);
       write(cg, y, inv);
       if (P.lse && cg == 0) P.lse[row] = (top + log2f(sum)) * kLn2;
     }

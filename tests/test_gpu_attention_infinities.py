@@ -32,3 +32,40 @@ def test_infinite_values_in_tiles_of_different_parts(lens, nodes, Hq, Hkv, dtype
     want = ta.ref(st)
     assert want[0][5, 0, 3] == float("inf") and want[0][200, 0, 3] == float("-inf")
     ta.close(out, lse, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("lens,nodes", [([0], [2]), ([20], [3]), ([5000], [3]), ([300] * 90, [5] * 90),
+                                        ([700] * 5, [200] * 5)])
+def test_rows_whose_scores_are_all_minus_infinity(lens, nodes, dtype):
+    """exp(-inf) is 0 for every key: the sum is 0, its logarithm -inf, and the
+    output 0 / 0, NaN; the other rows are those without it."""
+    st = ta.make(lens, nodes, 8, 4, 64, 16, dtype, "chain", seed=91)
+    for k in ("k", "k_cache"):
+        st[k][..., 0] = -1.0
+    base, blse = ta.check(st)
+    bad = dict(st, q=st["q"].clone())
+    hit = torch.zeros(base.shape[:2], dtype=torch.bool, device=DEV)
+    hit[1, 2] = hit[-1, 5] = True
+    bad["q"][..., 0][hit] = float("inf")
+    out, lse = sv.tree_attention(**bad, with_lse=True)
+    assert out[hit].isnan().all() and (lse[hit] == float("-inf")).all()
+    assert torch.equal(out[~hit], base[~hit]) and torch.equal(lse[~hit], blse[~hit])
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("lens,nodes", [([0], [2]), ([5000], [3]), ([700] * 5, [200] * 5)])
+def test_rows_with_an_infinite_or_undefined_score(lens, nodes, value):
+    """A score of +inf or NaN makes its row NaN, the others stay."""
+    st = ta.make(lens, nodes, 8, 4, 64, 16, "f16", "chain", seed=92)
+    for k in ("k", "k_cache"):
+        st[k][..., 0] = -1.0
+    st["k"][0, 0, 0] = 1.0  # +inf for an infinite query of the first key head
+    base, blse = ta.check(st)
+    bad = dict(st, q=st["q"].clone())
+    bad["q"][1, 1, 0] = value
+    out, lse = sv.tree_attention(**bad, with_lse=True)
+    hit = torch.zeros(base.shape[:2], dtype=torch.bool, device=DEV)
+    hit[1, 1] = True
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(out[~hit], base[~hit]) and torch.equal(lse[~hit], blse[~hit])
