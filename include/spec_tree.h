@@ -73,14 +73,16 @@ extern "C" {
  * Rule: token x at position i is accepted when u q(x) < p(x).  The first
  * rejection's correction token is drawn from max(p - q, 0) (from p with that
  * token's entry cleared, for point drafts); from p itself where that has no
- * mass; the bonus token, when all are accepted, from target row gamma.  The
- * draw from weights w is the lowest v whose cumulative weight exceeds
- * draw_uniform * sum(w).  Comparisons and sums are in fp64.
+ * mass (for point drafts: that token); the bonus token, when all are accepted,
+ * from target row gamma.  The draw from weights w is the lowest v whose
+ * cumulative weight exceeds draw_uniform * sum(w).  Comparisons and sums are in
+ * fp64.
  *
  * Marks (accept_len -1, tokens -1): a draft token outside [0, V), a uniform
  * outside [0, 1) or NaN, a drafted token's probability (target or draft) that
- * is negative or not finite, a sum of draw weights that is zero or not
- * finite.  Negative probabilities elsewhere weigh nothing.
+ * is negative or not finite, a sum of draw weights that is not finite or, with
+ * no point drafts to draw from instead, zero.  Negative probabilities elsewhere
+ * weigh nothing.
  */
 int spec_verify_probs(const void* target_probs, const void* draft_probs,
                       const int32_t* draft_tokens, const float* uniforms,
@@ -108,10 +110,12 @@ int spec_verify_probs(const void* target_probs, const void* draft_probs,
  * index order against the node's law r, r = p at first: child x is accepted
  * when u q(x) < r(x), and becomes the current node; after a rejection
  * r <- norm(max(r - q, 0)), unchanged where that has no mass (point drafts: r
- * loses the child's entry).  When no child is left the final token is drawn
- * from r.  After k rejections r = max(p - c_k q, 0) / M_k with c_0 = 0,
- * M_0 = 1, c_{k+1} = c_k + M_k and M_{k+1} = sum max(p - c_{k+1} q, 0), which
- * is how it is computed.
+ * loses the child's entry, and a token rejected once at a node is not accepted
+ * there again).  When no child is left the final token is drawn from r (point
+ * drafts that took all of its mass, possible where p sums to less than 1: the
+ * last of them that had any).  After k rejections r = max(p - c_k q, 0) / M_k
+ * with c_0 = 0, M_0 = 1, c_{k+1} = c_k + M_k and
+ * M_{k+1} = sum max(p - c_{k+1} q, 0), which is how it is computed.
  * Marks as spec_verify_probs (-1 in path too), and a sequence without nodes,
  * with more than max_nodes or SV_MAX_NODES of them, with a parent that does
  * not come before its node, with a second root, or whose cu_nodes bounds do

@@ -51,6 +51,7 @@ struct ProbsShared {
   double c, M;                  // the current law: max(p - c q, 0) / M
   int reduce;                   // the decision waits for the next residual's mass
   int cur, last, acc, ngone;    // current node, last child tried, accepted, rejected point drafts
+  int lost;                     // the last of those that had mass, or -1
   int bad, n;
   int64_t trow, drow, t0;  // first target row, draft row, token index
 };
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(kPThreads, 3) probs_kernel(const __grid_consta
     sh.last = 0;
     sh.acc = 0;
     sh.ngone = 0;
+    sh.lost = -1;
     sh.c = 0.0;
     sh.M = 1.0;
   }
@@ -301,9 +303,10 @@ __global__ void __launch_bounds__(kPThreads, 3) probs_kernel(const __grid_consta
   int held = -1;  // node whose current law csum and xsum hold
   int cur = 0;
   double total = 0.0;
+  int only = -1;  // the token to draw where the rejected point drafts left no mass
   while (ok) {
     if (warp == 0) {
-      int at = sh.cur, last = sh.last, acc = sh.acc, ngone = sh.ngone, need = 0;
+      int at = sh.cur, last = sh.last, acc = sh.acc, ngone = sh.ngone, lost = sh.lost, need = 0;
       double c = sh.c, M = sh.M;
       for (;;) {
         int child = n;
@@ -326,6 +329,7 @@ __global__ void __launch_bounds__(kPThreads, 3) probs_kernel(const __grid_consta
           yes = u * M < left;
           if (!yes) {
             M -= left;
+            if (left > 0.0) lost = ntok[child];
             if (lane == 0) gone[ngone] = ntok[child];
             __syncwarp();
             ++ngone;
@@ -336,6 +340,7 @@ __global__ void __launch_bounds__(kPThreads, 3) probs_kernel(const __grid_consta
           c = 0.0;
           M = 1.0;
           ngone = 0;
+          lost = -1;
           if (lane == 0) npath[acc] = child;
           ++acc;
         } else if (rows) {
@@ -348,6 +353,7 @@ __global__ void __launch_bounds__(kPThreads, 3) probs_kernel(const __grid_consta
         sh.last = last;
         sh.acc = acc;
         sh.ngone = ngone;
+        sh.lost = lost;
         sh.c = c;
         sh.M = M;
         sh.reduce = need;
@@ -373,7 +379,8 @@ __global__ void __launch_bounds__(kPThreads, 3) probs_kernel(const __grid_consta
       continue;
     }
     if (held != cur) total = reduce(cur, sh.c, sh.ngone);
-    ok = total > 0.0 && total < INFINITY;
+    if (total == 0.0) only = sh.lost;
+    ok = only >= 0 || (total > 0.0 && total < INFINITY);
     break;
   }
 
@@ -387,9 +394,12 @@ __global__ void __launch_bounds__(kPThreads, 3) probs_kernel(const __grid_consta
       for (int i = tid; i < P.width; i += kPThreads)
         opath[i] = i > acc ? -1 : (i == 0 ? 0 : npath[i - 1]);
     }
-    if (tid == 0) P.accept_len[b] = acc;
+    if (tid == 0) {
+      P.accept_len[b] = acc;
+      if (only >= 0) otok[acc] = only;
+    }
   }
-  if (!ok) return;
+  if (!ok || only >= 0) return;
 
   // The draw: the first entry whose cumulative weight exceeds t.  (Sums of
   // the same weights in another order may differ by a rounding: where that
