@@ -229,12 +229,9 @@ def kv_slots(lens, add, cu_rows, block_table, free_pages, free_count, *, rows: i
     return _call(dev, stream, body)
 
 
-def kv_append(k, v, slots, k_cache, v_cache, *, stream=None):
-    """Keys and values written into the paged cache: row i of k, v
-    [N, H, D] goes to slot slots[i] of k_cache, v_cache [pages, page_size, H,
-    D]; slots (int32) outside the cache skip the row.  With a leading layer
-    axis on all four, every layer at once.  Strides are free but for the last
-    axis; k, v must not overlap the caches.  Returns None."""
+def append_args(k, v, k_cache, v_cache):
+    """kv_append's rows and caches, checked, as its argument block without the
+    slots; None where there is nothing to copy."""
     dev, dt = _device(k), k.dtype
     shape = k.shape
     if len(shape) not in (3, 4):
@@ -244,24 +241,41 @@ def kv_append(k, v, slots, k_cache, v_cache, *, stream=None):
     pages, page = _dims(k_cache, "k_cache", len(shape) + 1)[-4:-2]
     cache = lead + (pages, page, H, D)
     _want(dev, (v, "v", dt, shape, False), (k_cache, "k_cache", dt, cache, False),
-          (v_cache, "v_cache", dt, cache, False), (slots, "slots", torch.int32, (N,), True))
+          (v_cache, "v_cache", dt, cache, False))
     es = k.element_size()
     if es not in (1, 2, 4):
         raise ValueError(f"elements of 1, 2 or 4 bytes are copied, got {k.dtype}")
     if k.numel() == 0 or k_cache.numel() == 0:
-        return
+        return None
     ks, vs, kcs, vcs = k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
     if D > 1 and not ks[-1] == vs[-1] == kcs[-1] == vcs[-1] == 1:
         raise ValueError("the last axis of k, v and the caches must be contiguous")
     two = _i64 * 2
     layered = bool(lead)
-    a = _AppendArgs(
+    return _AppendArgs(
         (_vp * 2)(k.data_ptr(), v.data_ptr()), (_vp * 2)(k_cache.data_ptr(), v_cache.data_ptr()),
         two(ks[0], vs[0]) if layered else two(), two(ks[-3], vs[-3]), two(ks[-2], vs[-2]),
         two(kcs[0], vcs[0]) if layered else two(), two(kcs[-4], vcs[-4]), two(kcs[-3], vcs[-3]),
-        two(kcs[-2], vcs[-2]), slots.data_ptr(), lead[0] if layered else 1, N, H, D, pages, page,
-        es)
-    _call(dev, stream, lambda s: _check(_lib().spec_kv_append(C.byref(a), s)))
+        two(kcs[-2], vcs[-2]), None, lead[0] if layered else 1, N, H, D, pages, page, es)
+
+
+def append_rows(args, slots, device, stream):
+    """kv_append of checked arguments."""
+    if args is None:
+        return
+    args.slots = slots.data_ptr()
+    _call(device, stream, lambda s: _check(_lib().spec_kv_append(C.byref(args), s)))
+
+
+def kv_append(k, v, slots, k_cache, v_cache, *, stream=None):
+    """Keys and values written into the paged cache: row i of k, v
+    [N, H, D] goes to slot slots[i] of k_cache, v_cache [pages, page_size, H,
+    D]; slots (int32) outside the cache skip the row.  With a leading layer
+    axis on all four, every layer at once.  Strides are free but for the last
+    axis; k, v must not overlap the caches.  Returns None."""
+    args = append_args(k, v, k_cache, v_cache)
+    _want(k.device, (slots, "slots", torch.int32, (k.shape[-3],), True))
+    append_rows(args, slots, k.device, stream)
 
 
 def tree_attention_workspace_size(Hq: int, Hkv: int, D: int) -> int:

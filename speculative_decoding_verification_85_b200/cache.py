@@ -15,7 +15,9 @@ from __future__ import annotations
 
 import torch
 
-from ._tree import kv_append, kv_slots, tree_attention, tree_attention_workspace_size
+from ._tree import (
+    append_args, append_rows, kv_slots, tree_attention, tree_attention_workspace_size,
+)
 
 
 class PagedCache:
@@ -53,12 +55,14 @@ class PagedCache:
         """The first add[b] packed rows of every request (or those that `path`
         names) of k, v [layers, N, kv_heads, head_dim] join the cache.  Returns
         start [batch]: the position of the first new token, -1 where there was
-        no room (the request stays as it was)."""
+        no room (the request stays as it was).  Rows that do not fit the caches
+        raise before anything changes."""
+        args = append_args(k, v, self.k, self.v)  # refused, if at all, before anything changes
         slots, start, _, _ = kv_slots(self.lens, add, cu_rows, self.block_table, self.free_pages,
                                       self.free_count, rows=k.shape[1], page_size=self.page_size,
                                       path=path, out_lens=self.lens,
                                       out_free_count=self.free_count, stream=stream)
-        kv_append(k, v, slots, self.k, self.v, stream=stream)
+        append_rows(args, slots, k.device, stream)
         return start
 
     def commit(self, k, v, cu_nodes, accept_len, path=None, *, stream=None):
