@@ -23,14 +23,16 @@
 // maximum has grown by more than 2^8; until then weights up to 2^8 (fp16: 2^15,
 // see kHold) are accumulated, which fp32 holds as well.
 //
-// Bound by memory up to about 250 query rows a key head.  Measured (1.08 GB of
-// keys and values, 64 x 4096 tokens, 8 key heads of 128, pages of 128): 176 us
-// with 4 rows a key head (0.93 of the measured copy bandwidth), 201 us with
-// 128, 314 us with 256 (two groups of 128 exponentials a key each): there the
-// chain scores -> weights -> accumulator -> next scores of a group sets the
-// pace, at half of the tensor pipe and of the special function units.  Pages of
-// 16 cost 4% more than pages of 128 (eight loads a tile and 64 columns; 9% with
-// one loading warp for both column halves).
+// Bound by memory while a key head has one tile of query rows.  Measured (1.08 GB
+// of keys and values, 64 x 4096 tokens, 8 key heads of 128, pages of 128): 182 us
+// with 4 rows a key head (0.90 of the measured copy bandwidth), 188 with 20, 210
+// with 128 (0.79), 335 with 256 (two groups of 128 exponentials a key each):
+// there the chain scores -> weights -> accumulator -> next scores of a group sets
+// the pace, and products and exponentials take turns, at half of the tensor pipe
+// and of the special function units.  Pages of 16 take the same 188 us with 20
+// rows.  Contexts of 1 to 8192 tokens with as many bytes take 203: the line is
+// cut by a count of tiles, in which a partial tile stands for a whole one and the
+// start and end of a unit for nothing.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -299,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
   // ---- where this CTA's stretch begins: prefix sums of the sequences' tiles.  The key warp
   // alone walks the line; for a few sequences it also finds the start alone, while the others
-  // set up, else the whole block does.
+  // set up, else the whole block does.  (One node and 100 tokens a sequence, key warp / block:
+  // 1 sequence 10.7 / 11.4 us, 16: 11.9 / 12.6, 64: 12.5 / 12.3, 128: 18.2 / 16.1, 256: 32 / 26.)
   const bool few = P.B <= 128;
   auto find_start = [&](auto wide) {
     constexpr bool kWide = decltype(wide)::value;
@@ -919,9 +922,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 // Join of the units that CTA borders cut.  Every block lists the cut units
 // (one for each CTA at most) and takes its share of their items: 32 rows, a
 // warp an eighth of the columns, or, where a unit has eight parts or more, 32
-// rows by one group of four columns, a warp an eighth of the parts.  Bound by
-// the parts' bytes, so a lane has several loads in flight; parts are added in a
-// fixed order.
+// rows by one group of four columns, a warp an eighth of the parts.  (26 nodes of
+// 8 heads, the whole call, parts split over warps / not: 37 parts a unit 95 / 98
+// us, 18: 96 / 95, 9: 175 / 173, 5: 183 / 178, 2: 232 / 185.)  Bound by the parts'
+// bytes, so a lane has several loads in flight; parts are added in a fixed order.
 constexpr int kJoinThreads = 256;
 
 // Adds parts p, p + step, ... (kAt of them at a time, loaded together) of kGroups column groups;
@@ -1126,23 +1130,6 @@ AttnLayout attn_layout(int D) {
   return l;
 }
 
-int sm_count(int* out) {
-  static std::mutex mu;
-  static int cached[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-  std::lock_guard<std::mutex> lk(mu);
-  int n = dev >= 0 && dev < 64 ? cached[dev] : 0;
-  if (n == 0) {
-    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return set_error(SV_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
-    if (dev >= 0 && dev < 64) cached[dev] = n;
-  }
-  *out = n < kMaxCtas ? n : kMaxCtas;
-  return SV_OK;
-}
-
 template <int DP, bool kBf16>
 int launch_attn(const AttnParams& p, int ctas, cudaStream_t stream) {
   constexpr size_t kSmem = Shape<DP>::kTiles + sizeof(Shared);
@@ -1225,8 +1212,7 @@ int spec_tree_attention(const sv_tree_attention_args* a, void* workspace, size_t
     return set_error(SV_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes, lay.total);
   int rc = check_device();
   if (rc != SV_OK) return rc;
-  int ctas = 0;
-  if ((rc = sm_count(&ctas)) != SV_OK) return rc;
+  const int ctas = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
   const EncodeFn enc = encoder();
   if (!enc) return set_error(SV_ERR_CUDA, "the driver offers no cuTensorMapEncodeTiled");
 

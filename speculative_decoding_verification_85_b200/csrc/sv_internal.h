@@ -92,6 +92,7 @@ int check_device();
 int check_launch(const char* what);
 // Once per kernel and device: allow `smem` bytes of dynamic shared memory.
 int allow_smem(const void* kernel, size_t smem);
+int sm_count();  // SMs of the current device (sv_single.cu)
 
 // Kernel launchers (sv_single.cu / sv_multi.cu).
 int launch_single(const void* target, const void* draft, const int32_t* tokens,

@@ -144,7 +144,10 @@ __device__ __forceinline__ int slot_of(const SlotParams& P, int b, int row) {
 // pages (every block runs the same sums; the first one writes the requests'
 // outputs, which may be their inputs, once all have read), and
 // slots_rows_kernel does the rows: 512 prompts, 10^6 rows and 66,000 pages
-// took 67 us with one block.
+// took 67 us with one block, and take 20.  The border is where one block's time
+// reaches that of a call from Python (device, call): 64 requests, 1,024 rows 6.4,
+// 19 us with one block, 9.4, 20 with the cluster; 8,192 rows 13.7, 18 and 9.5, 20;
+// 16,384 rows 22, 23 and 9.6, 20.
 constexpr int kSlotCtas = 8;
 template <bool kMany>
 __global__ void __launch_bounds__(kSThreads) slots_kernel(const SlotParams P) {
@@ -301,7 +304,7 @@ template <typename T>
 void launch_append(AppendParams p, int head_bytes, cudaStream_t stream) {
   p.vecs = head_bytes / static_cast<int>(sizeof(T));
   const int64_t blocks = (p.units + kAThreads / 32 - 1) / (kAThreads / 32);
-  append_kernel<T><<<static_cast<unsigned>(std::min<int64_t>(blocks, 148 * 8)), kAThreads, 0, stream>>>(p);
+  append_kernel<T><<<static_cast<unsigned>(std::min<int64_t>(blocks, sm_count() * 8)), kAThreads, 0, stream>>>(p);
 }
 
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }

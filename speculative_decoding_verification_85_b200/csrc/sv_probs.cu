@@ -7,14 +7,16 @@
 // c_{k+1} = c_k + M_k, M_{k+1} = sum max(p - c_{k+1} q, 0)), so each
 // rejection costs one sum over the row pair and nothing is written.
 //
-// The draw: every CTA of the cluster sums its slice of the row in chunks of
-// 512 entries (one warp a chunk, 16 entries a lane in flight), the slices'
-// sums are exchanged through distributed shared memory, every CTA finds the
-// slice that the uniform falls into, and one warp of that CTA walks down its
-// chunk sums and one chunk again (from L2).  256 chains of 4 at V = 151936 fp32
-// take 53 us: 0.86 of the measured copy bandwidth.  Sums are fp64: the order of
-// addition then moves a border by 1e-16 of the mass, so the drawn entry is
-// the one of the definition.
+// The sums: every CTA of the cluster sums its slice of the row in chunks of
+// 512 entries, a warp a chunk.  A residual over aligned rows takes two chunks of
+// both rows at a time (64 entries a lane in flight); plain rows, unaligned ones
+// and a slice's last chunks go one chunk at a time.  The slices' sums are
+// exchanged through distributed shared memory, every CTA finds the slice that
+// the uniform falls into, and one warp of that CTA walks down its chunk sums and
+// one chunk again (from L2).  256 chains of 4 at V = 151936 fp32 take 54 us: 0.83
+// of the measured copy bandwidth.  Sums are fp64: the order of addition then
+// moves a border by 1e-16 of the mass, so the drawn entry is the one of the
+// definition.
 #include <cuda_runtime.h>
 
 #include "spec_tree.h"
@@ -493,7 +495,7 @@ int launch_probs(ProbsParams p, int B, cudaStream_t stream) {
   // 20 us with four CTAs each, 25 with eight; 128: 30 with two, 37 with four; 256: 53 with one,
   // 61 with two.  V = 128256 bf16 trees of 21 nodes: 64 sequences 31 us with eight, 32 with four,
   // 45 with two.)
-  const int limit = (p.tree && p.draft ? 8 : 3) * 148;
+  const int limit = (p.tree && p.draft ? 8 : 3) * sm_count();
   int C = 1;
   while (C < kMaxCluster && B * C * 2 <= limit && nch > C * kPWarps) C *= 2;
   p.cluster = C;

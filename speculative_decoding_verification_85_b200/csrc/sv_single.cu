@@ -903,6 +903,8 @@ int per_device(std::atomic<int> (&slots)[64], int fallback, Query query) {
   return v;
 }
 
+}  // namespace
+
 int sm_count() {
   static std::atomic<int> slots[64];
   return per_device(slots, 148, [](int dev) {
@@ -915,6 +917,7 @@ int sm_count() {
   });
 }
 
+namespace {
 template <typename Kernel>
 int occupancy(Kernel kernel, int threads) {
   int n = 0;
